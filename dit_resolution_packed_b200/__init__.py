@@ -14,9 +14,12 @@ import math
 import os
 import re
 
+from . import block
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libpackattn.so")
 HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "packattn.h")
+BLOCK_HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "packattn_block.h")
 
 PA_OK = 0
 PA_ERR_NULL = -1
@@ -30,6 +33,9 @@ PA_ERR_CUDA = -8
 PA_ERR_SCALE = -9
 PA_ERR_NOT_DEVICE = -10
 PA_ERR_NOALLOC_LIMIT = -11
+PA_ERR_WORKSPACE = -12
+PA_ERR_BLOCKS = -13
+PA_ERR_MODE = -14
 NOALLOC_MAX_BATCH = 1024
 
 _lib = None
@@ -92,6 +98,7 @@ def load_library(path=None):
     lib.pa_profile_enable.argtypes = [ctypes.c_int]
     lib.pa_profile_read.restype = ctypes.c_int
     lib.pa_profile_read.argtypes = [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_int32)]
+    block.declare(lib)
     if path is None:
         _lib = lib
     return lib
@@ -443,3 +450,8 @@ def pa_profile_read():
     if rc != PA_OK:
         raise PackAttnError(rc, "pa_profile_read")
     return ms.value, n.value
+
+
+# the block around the attention and its sparse form (include/packattn_block.h)
+from .block import (  # noqa: E402
+    block_norm_bwd, block_norm_fwd, pa_block_norm_bwd, pa_block_norm_fwd, pa_block_norm_workspace_bytes)

@@ -12,22 +12,22 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libpackattn.so")
-SOURCES = ["packattn.cu"]
+SOURCES = ["packattn.cu", "block_norm.cu"]
 HEADERS = ["sm100_ptx.cuh", "schedule.cuh", "attn_fwd_sm100.cuh", "attn_fwd_fp8_sm100.cuh", "attn_bwd_sm100.cuh",
-           "gemm_sm100.cuh", "exp2_poly.cuh"]
+           "gemm_sm100.cuh", "exp2_poly.cuh", "host.h", "block_norm_sm100.cuh"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
 def _inputs():
     files = [os.path.join(CSRC, f) for f in SOURCES + HEADERS]
-    files.append(os.path.join(ROOT, "include", "packattn.h"))
+    files += [os.path.join(ROOT, "include", h) for h in ("packattn.h", "packattn_block.h")]
     files.append(os.path.abspath(__file__))
     return files
 
 
 def nvcc_command(out=LIB, extra=()):
-    return [NVCC, *ARCH, "-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr",
+    return [NVCC, *ARCH, "-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr", "--threads", "4",
             "-Xcompiler", "-fPIC,-fvisibility=hidden", "-shared", "-cudart", "static",
             "-Xlinker", "--exclude-libs,ALL", "-Xlinker", "-Bsymbolic",
             "-I", os.path.join(ROOT, "include"), "-I", CSRC,

@@ -1,0 +1,190 @@
+"""Binding of ``include/packattn_block.h``: what stands around and inside the packed attention in a DiT block.
+
+As in the package's other bindings, the functions named ``pa_*`` mirror the C ABI and only marshal arguments;
+the others allocate outputs and scratch memory, call them and raise on a host-side error status.  Outputs and
+scratch come from torch's allocator under ``stream`` (default: the current stream of the tensors' device), so
+they may be freed or captured into a graph like any other tensor of that stream.
+"""
+import contextlib
+import ctypes
+import math
+
+NORM_KINDS = {"none": 0, "layer": 1, "rms": 2}
+
+
+class BlockNormDesc(ctypes.Structure):
+    """``pa_block_norm_desc``."""
+    _fields_ = [("total_tokens", ctypes.c_int32), ("batch", ctypes.c_int32), ("hidden", ctypes.c_int32),
+                ("residual_fp32", ctypes.c_int32), ("param_fp32", ctypes.c_int32), ("post", ctypes.c_int32),
+                ("pre", ctypes.c_int32), ("residual_scale", ctypes.c_float), ("eps", ctypes.c_float),
+                ("cu_seqlens", ctypes.c_void_p), ("gate", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+                ("shift", ctypes.c_void_p), ("gate_stride", ctypes.c_int64), ("scale_stride", ctypes.c_int64),
+                ("shift_stride", ctypes.c_int64), ("w_post", ctypes.c_void_p), ("w_pre", ctypes.c_void_p)]
+
+
+def declare(lib):
+    """Sets the argument types of the header's functions on a loaded library."""
+    vp, i32, i64, f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
+    norm = ctypes.POINTER(BlockNormDesc)
+    for name, res, args in (
+            ("pa_block_norm_fwd", ctypes.c_int, [norm, vp, vp, vp, vp, vp]),
+            ("pa_block_norm_workspace_bytes", i64, [i32, i32, i32]),
+            ("pa_block_norm_bwd", ctypes.c_int, [norm] + [vp] * 12 + [i64, vp])):
+        fn = getattr(lib, name)
+        fn.restype, fn.argtypes = res, args
+
+
+def _library():
+    import dit_resolution_packed_b200 as pa
+    return pa.load_library()
+
+
+def _raise_on(rc, where):
+    if rc != 0:
+        import dit_resolution_packed_b200 as pa
+        raise pa.PackAttnError(rc, where)
+
+
+def _handle(stream, like):
+    """cudaStream_t of ``stream``, or of the current stream of the device that ``like`` lives on."""
+    import torch
+    if stream is None:
+        if not like.is_cuda:
+            return None  # the call refuses host memory
+        stream = torch.cuda.current_stream(like.device)
+    return stream.cuda_stream
+
+
+def _under(stream):
+    import torch
+    return torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
+
+
+def _p(t):
+    return None if t is None else t.data_ptr()
+
+
+def _check(dtype, shape, **tensors):
+    """Each given tensor is contiguous, of this type and (unless None) of this shape."""
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if shape is not None and tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+
+
+# ---------------------------------------------------------------- norms, gate and residual
+
+def _norm_desc(like, cu_seqlens, gate, post, w_post, residual_scale, pre, w_pre, scale, shift, eps):
+    import torch
+    if like.dim() != 2:
+        raise ValueError("the residual stream must be [T, C]")
+    T, C = like.shape
+    if like.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"the residual stream must be bfloat16 or float32, got {like.dtype}")
+    if post not in NORM_KINDS or pre not in NORM_KINDS:
+        raise ValueError(f"post and pre must be one of {sorted(NORM_KINDS)}")
+    given = {"gate": gate, "scale": scale, "shift": shift, "w_post": w_post, "w_pre": w_pre}
+    types = {t.dtype for t in given.values() if t is not None}
+    if len(types) > 1 or not types <= {torch.bfloat16, torch.float32}:
+        raise TypeError("gate, scale, shift and the weights must be all bfloat16 or all float32")
+    B = 0
+    if cu_seqlens is not None:
+        _check(torch.int32, None, cu_seqlens=cu_seqlens)
+        B = cu_seqlens.numel() - 1
+    for name in ("gate", "scale", "shift"):
+        t = given[name]
+        if t is None:
+            continue
+        if cu_seqlens is None:
+            raise ValueError(f"{name} needs cu_seqlens")
+        if tuple(t.shape) != (B, C) or (C > 1 and t.stride(1) != 1):
+            raise ValueError(f"{name} must be [B, C] with contiguous rows")
+    for name in ("w_post", "w_pre"):
+        t = given[name]
+        if t is not None and (tuple(t.shape) != (C,) or not t.is_contiguous()):
+            raise ValueError(f"{name} must be [C], contiguous")
+    if cu_seqlens is None:
+        B = 1  # one segment over all tokens: nothing reads it
+    stride = [t.stride(0) if t is not None else 0 for t in (gate, scale, shift)]
+    return BlockNormDesc(T, B, C, int(like.dtype == torch.float32), int(types == {torch.float32}), NORM_KINDS[post],
+                         NORM_KINDS[pre], residual_scale, eps, _p(cu_seqlens), _p(gate), _p(scale), _p(shift),
+                         *stride, _p(w_post), _p(w_pre))
+
+
+def pa_block_norm_workspace_bytes(batch, total_tokens, hidden):
+    """C ``pa_block_norm_workspace_bytes``."""
+    return int(_library().pa_block_norm_workspace_bytes(int(batch), int(total_tokens), int(hidden)))
+
+
+def pa_block_norm_fwd(x, cu_seqlens, y, r, z, *, gate=None, post="none", w_post=None, residual_scale=1.0, pre="none",
+                      w_pre=None, scale=None, shift=None, eps=1e-6, stream=None):
+    """C ``pa_block_norm_fwd``: x, r [T, C] (bf16 or fp32), y, z bf16 [T, C], gate, scale, shift [B, C] (rows may be
+    strided), weights [C]; y, r and z may be None as the header says.  Returns the status code."""
+    import torch
+    desc = _norm_desc(x, cu_seqlens, gate, post, w_post, residual_scale, pre, w_pre, scale, shift, eps)
+    _check(x.dtype, x.shape, x=x, r=r)
+    _check(torch.bfloat16, x.shape, y=y, z=z)
+    return _library().pa_block_norm_fwd(ctypes.byref(desc), _p(x), _p(y), _p(r), _p(z), _handle(stream, x))
+
+
+def block_norm_fwd(x, cu_seqlens=None, *, y=None, gate=None, post="none", w_post=None, residual_scale=1.0,
+                   pre="layer", w_pre=None, scale=None, shift=None, eps=1e-6, stream=None):
+    """The join between two blocks: r = residual_scale x + gate[s] N_post(y) w_post, and the next block's input
+    z = N_pre(r) w_pre (1 + scale[s]) + shift[s], s being the image of a token.
+
+    x [T, C] bf16 or fp32; y bf16 [T, C] (None: no join, r is x); gate, scale, shift [B, C] and weights [C], each
+    optional; post and pre "none", "layer" or "rms".  Returns (r of x's type, z bf16, or None with pre "none")."""
+    import torch
+    with _under(stream):
+        r = torch.empty_like(x) if y is not None else None
+        z = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device) if pre != "none" else None
+    rc = pa_block_norm_fwd(x, cu_seqlens, y, r, z, gate=gate, post=post, w_post=w_post, residual_scale=residual_scale,
+                           pre=pre, w_pre=w_pre, scale=scale, shift=shift, eps=eps, stream=stream)
+    _raise_on(rc, "pa_block_norm_fwd")
+    return (x if y is None else r), z
+
+
+def pa_block_norm_bwd(r, cu_seqlens, y, dr, dz, dx, dy, dgate, dscale, dshift, dw_post, dw_pre, workspace, *,
+                      gate=None, post="none", w_post=None, residual_scale=1.0, pre="none", w_pre=None, scale=None,
+                      shift=None, eps=1e-6, stream=None):
+    """C ``pa_block_norm_bwd``: r, dr, dx [T, C] of the residual's type, y, dz, dy bf16 [T, C], dgate, dscale, dshift
+    fp32 [B, C], dw_post, dw_pre fp32 [C], workspace a byte tensor; None as the header says."""
+    import torch
+    desc = _norm_desc(r, cu_seqlens, gate, post, w_post, residual_scale, pre, w_pre, scale, shift, eps)
+    _check(r.dtype, r.shape, r=r, dr=dr, dx=dx)
+    _check(torch.bfloat16, r.shape, y=y, dz=dz, dy=dy)
+    _check(torch.float32, (desc.batch, desc.hidden), dgate=dgate, dscale=dscale, dshift=dshift)
+    _check(torch.float32, (desc.hidden,), dw_post=dw_post, dw_pre=dw_pre)
+    return _library().pa_block_norm_bwd(
+        ctypes.byref(desc), _p(r), _p(y), _p(dr), _p(dz), _p(dx), _p(dy), _p(dgate), _p(dscale), _p(dshift),
+        _p(dw_post), _p(dw_pre), _p(workspace), 0 if workspace is None else workspace.numel(), _handle(stream, r))
+
+
+def block_norm_bwd(r, cu_seqlens=None, dr=None, dz=None, *, y=None, gate=None, post="none", w_post=None,
+                   residual_scale=1.0, pre="layer", w_pre=None, scale=None, shift=None, eps=1e-6, stream=None):
+    """Gradients of ``block_norm_fwd`` from its r (x where there was no join), dr = dL/dr (or None) and dz = dL/dz,
+    with the forward's other arguments.  Returns a dict with dx and, each None where the forward had no such input,
+    dy, dgate, dscale, dshift (fp32 [B, C]), dw_post, dw_pre (fp32 [C])."""
+    import torch
+    C = r.shape[1]
+    f32 = dict(dtype=torch.float32, device=r.device)
+    with _under(stream):
+        out = dict(dx=torch.empty_like(r), dy=torch.empty_like(y) if y is not None else None)
+        for name, t in (("dgate", gate), ("dscale", scale), ("dshift", shift), ("dw_post", w_post), ("dw_pre", w_pre)):
+            out[name] = torch.empty(t.shape, **f32) if t is not None else None
+        ws = None
+        if any(t is not None for t in (gate, scale, shift, w_post, w_pre)):
+            B = cu_seqlens.numel() - 1 if cu_seqlens is not None else 1
+            ws = torch.empty(max(pa_block_norm_workspace_bytes(B, r.shape[0], C), 0), dtype=torch.uint8,
+                             device=r.device)
+    rc = pa_block_norm_bwd(r, cu_seqlens, y, dr, dz, out["dx"], out["dy"], out["dgate"], out["dscale"], out["dshift"],
+                           out["dw_post"], out["dw_pre"], ws, gate=gate, post=post, w_post=w_post,
+                           residual_scale=residual_scale, pre=pre, w_pre=w_pre, scale=scale, shift=shift, eps=eps,
+                           stream=stream)
+    _raise_on(rc, "pa_block_norm_bwd")
+    return out

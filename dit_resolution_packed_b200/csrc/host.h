@@ -1,0 +1,46 @@
+// host.h -- host-side services of the library that its entry points in several source files share:
+// argument checks, the device and stream of a call, the status word, tensor-map encoding.  Defined in
+// packattn.cu (nothing here is exported from the library).
+#pragma once
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <initializer_list>
+
+namespace pa {
+namespace host {
+
+inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+// PA_OK with `*dev` set when every non-null pointer is memory of one GPU, else PA_ERR_NOT_DEVICE.
+int common_device(std::initializer_list<const void*> ptrs, int* dev);
+
+// One enqueueing call: holds the library's lock, makes the buffers' device current (the thread's own one is
+// put back at the end) and finds the status word of (device, stream).  rc is not PA_OK when that failed.
+class Call {
+ public:
+  Call(int dev, void* stream);
+  ~Call();
+  Call(const Call&) = delete;
+  Call& operator=(const Call&) = delete;
+
+  int rc;
+  int sms = 0;
+  cudaStream_t stream;
+  int32_t* status = nullptr;
+  uint64_t wait_limit_ns = 0;
+
+ private:
+  int prev_dev_ = -1;
+};
+
+// Tensor map of a bf16 [rows, heads * head_dim] matrix, box 64 columns x 128 rows, 128-byte swizzle.
+bool encode_rows(CUtensorMap* m, const void* base, int32_t rows, int32_t heads, int32_t head_dim);
+// Tensor map of a bf16 row-major [outer, inner] matrix, box {64, box_outer}, 128-byte swizzle.
+bool encode_matrix(CUtensorMap* m, const void* base, int64_t inner, int64_t outer, uint32_t box_outer);
+
+inline int launch_status() { return cudaGetLastError() == cudaSuccess ? 0 : -8; }
+
+}  // namespace host
+}  // namespace pa

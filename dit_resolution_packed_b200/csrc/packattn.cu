@@ -19,7 +19,8 @@
 #include "attn_fwd_fp8_sm100.cuh"
 #include "attn_fwd_sm100.cuh"
 #include "gemm_sm100.cuh"
-#include "packattn.h"
+#include "host.h"
+#include "packattn_block.h"
 #include "schedule.cuh"
 
 namespace {
@@ -115,6 +116,25 @@ StreamState* state_for(int device, cudaStream_t stream) {
 
 int ensure_status(StreamState* s) {
   if (s->status) return PA_OK;
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(s->stream, &capture) != cudaSuccess) return PA_ERR_CUDA;
+  if (capture != cudaStreamCaptureStatusNone) {
+    // A stream-ordered allocation made here would belong to the graph; the word has to outlive it.  So it is
+    // allocated and cleared outside the capture, on a stream of its own.
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) return PA_ERR_CUDA;
+    int32_t* word = nullptr;
+    cudaStream_t side = nullptr;
+    const bool ok = cudaStreamCreateWithFlags(&side, cudaStreamNonBlocking) == cudaSuccess &&
+                    cudaMalloc(reinterpret_cast<void**>(&word), 128) == cudaSuccess &&
+                    cudaMemsetAsync(word, 0, 128, side) == cudaSuccess && cudaStreamSynchronize(side) == cudaSuccess;
+    if (side) cudaStreamDestroy(side);
+    if (!ok && word) cudaFree(word);
+    cudaThreadExchangeStreamCaptureMode(&mode);
+    if (!ok) return PA_ERR_CUDA;
+    s->status = word;
+    return PA_OK;
+  }
   if (cudaMallocAsync(reinterpret_cast<void**>(&s->status), 128, s->stream) != cudaSuccess) return PA_ERR_CUDA;
   if (cudaMemsetAsync(s->status, 0, 128, s->stream) != cudaSuccess) return PA_ERR_CUDA;
   return PA_OK;
@@ -173,7 +193,7 @@ bool encode_map(CUtensorMap* m, const void* base, int32_t rows, int32_t heads, i
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+using pa::host::aligned;
 
 // A bf16 row-major [outer, inner] matrix, box {64, box_outer}, 128-byte swizzle.
 bool encode_2d(CUtensorMap* m, const void* base, int64_t inner, int64_t outer, uint32_t box_outer) {
@@ -321,6 +341,55 @@ BwdWsLayout bwd_ws_layout(int32_t batch, int32_t total, int32_t heads, int32_t h
 }
 
 }  // namespace
+
+// ---- services for the entry points in the other source files (host.h)
+namespace pa {
+namespace host {
+
+int common_device(std::initializer_list<const void*> ptrs, int* dev) {
+  int found = -1;
+  for (const void* p : ptrs) {
+    if (!p) continue;
+    int d = -1;
+    const int rc = device_of(p, &d);
+    if (rc != PA_OK) return rc;
+    if (found >= 0 && d != found) return PA_ERR_NOT_DEVICE;
+    found = d;
+  }
+  if (found < 0) return PA_ERR_NOT_DEVICE;
+  *dev = found;
+  return PA_OK;
+}
+
+Call::Call(int dev, void* stream_handle) : rc(PA_OK), stream(static_cast<cudaStream_t>(stream_handle)) {
+  g_mu.lock();
+  if (cudaGetDevice(&prev_dev_) != cudaSuccess || (prev_dev_ != dev && cudaSetDevice(dev) != cudaSuccess)) {
+    rc = PA_ERR_CUDA;
+    return;
+  }
+  if ((rc = ensure_device(dev)) != PA_OK) return;
+  StreamState* st = state_for(dev, stream);
+  if ((rc = ensure_status(st)) != PA_OK) return;
+  sms = g_dev[dev].sms;
+  status = st->status;
+  wait_limit_ns = static_cast<uint64_t>(g_wait_limit_ms) * 1000000ull;
+}
+
+Call::~Call() {
+  int now = -1;
+  if (prev_dev_ >= 0 && cudaGetDevice(&now) == cudaSuccess && now != prev_dev_) cudaSetDevice(prev_dev_);
+  g_mu.unlock();
+}
+
+bool encode_rows(CUtensorMap* m, const void* base, int32_t rows, int32_t heads, int32_t head_dim) {
+  return encode_map(m, base, rows, heads, head_dim);
+}
+bool encode_matrix(CUtensorMap* m, const void* base, int64_t inner, int64_t outer, uint32_t box_outer) {
+  return encode_2d(m, base, inner, outer, box_outer);
+}
+
+}  // namespace host
+}  // namespace pa
 
 // ---- scratch of pa_varlen_attn_fwd_noalloc ----------------------------------
 // One fixed array in the library's device image: the status word (bytes
@@ -689,6 +758,9 @@ const char* pa_status_string(int code) {
     case PA_ERR_CUDA: return "CUDA runtime error";
     case PA_ERR_SCALE: return "scale is not finite";
     case PA_ERR_NOT_DEVICE: return "a buffer is not device memory of one GPU";
+    case PA_ERR_WORKSPACE: return "the workspace is missing, misaligned (16 bytes) or too small";
+    case PA_ERR_BLOCKS: return "a block list is not increasing, leaves its segment, or is too long";
+    case PA_ERR_MODE: return "a norm kind or a combination of given and missing buffers that the call does not have";
     case PA_ERR_NOALLOC_LIMIT: return "batch exceeds the 1024 segments of pa_varlen_attn_fwd_noalloc's fixed scratch";
     default: return "unknown status";
   }

@@ -1,0 +1,106 @@
+/*
+ * packattn_block.h -- C ABI of what stands around and inside the packed attention in a DiT block
+ * (same library as packattn.h, whose status codes, conventions and pa_get_error it shares):
+ *
+ *   pa_block_norm_fwd / _bwd         gated residual join with the norm behind a block and the norm in
+ *                                    front of the next
+ *
+ * Unlike packattn.h's entry points these take their scratch memory from the caller, so that two captured
+ * graphs, or two streams, that use different buffers never share one; the library itself holds only the
+ * status word of the (device, stream) pair.  None of them synchronises or allocates on the device after
+ * the first call on a stream, each may be captured into a CUDA graph, and each leaves the calling
+ * thread's current device as it was.
+ */
+#ifndef PACKATTN_BLOCK_H_
+#define PACKATTN_BLOCK_H_
+
+#include "packattn.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* Further status codes (see enum pa_status). */
+enum pa_block_status {
+  PA_ERR_WORKSPACE = -12, /* the workspace is NULL, misaligned or too small */
+  PA_ERR_BLOCKS = -13,    /* a list of key blocks is not increasing, leaves its segment, or is too long */
+  PA_ERR_MODE = -14       /* a norm kind, or a combination of given and missing buffers, that the call does not have */
+};
+
+enum pa_norm_kind {
+  PA_NORM_NONE = 0,
+  PA_NORM_LAYER = 1, /* (v - mean) / sqrt(mean((v - mean)^2) + eps) over the channels */
+  PA_NORM_RMS = 2    /* v / sqrt(mean(v^2) + eps) */
+};
+
+/*
+ * The join between two blocks of a packed stream x [total_tokens, hidden], with s the segment (image) of a
+ * token:
+ *     u = N_post(y) * w_post                          (the block's output y behind its norm)
+ *     r = residual_scale * x + gate[s] * u            (stored in the residual's type)
+ *     z = N_pre(r) * w_pre * (1 + scale[s]) + shift[s]   (the next block's input)
+ * N_pre is taken of r as it is stored.  A NULL gate, weight or scale counts as 1 (scale: as 0), a NULL shift
+ * as 0.  Statistics, sums and products are fp32; r and z are rounded once each.
+ *
+ *   total_tokens, batch, cu_seqlens   the pack, as for pa_varlen_attn_fwd; cu_seqlens is read (and may only
+ *                     be NULL if it is not) when gate, scale or shift is given.
+ *   hidden            channels, a multiple of 8, 8 .. 8192.
+ *   residual_fp32     type of x, r, dr, dx: 1 fp32, 0 bf16.  y, z, dy, dz are bf16.
+ *   param_fp32        type of gate, scale, shift, w_post, w_pre: 1 fp32, 0 bf16.
+ *   post, pre         enum pa_norm_kind of N_post and N_pre.
+ *   gate_stride, scale_stride, shift_stride   elements from one segment's row of [batch, hidden] to the next
+ *                     (slices of one projection's output; 0: one row for all); rows 16-byte aligned.
+ * Every buffer is 16-byte aligned (cu_seqlens 4-byte), on one device, and token rows are contiguous.
+ */
+typedef struct pa_block_norm_desc {
+  int32_t total_tokens, batch, hidden;
+  int32_t residual_fp32, param_fp32;
+  int32_t post, pre;
+  float residual_scale, eps;
+  const int32_t* cu_seqlens;
+  const void* gate;
+  const void* scale;
+  const void* shift;
+  int64_t gate_stride, scale_stride, shift_stride;
+  const void* w_post;
+  const void* w_pre;
+} pa_block_norm_desc;
+
+/*
+ * pa_block_norm_fwd -- enqueue the join on `stream`.
+ *   y NULL: no join, z is the norm of x; then r is NULL, residual_scale 1, post NONE, and w_post and gate NULL.
+ *   z NULL: no norm in front; then pre is NONE, and w_pre, scale and shift NULL.  pre NONE needs z NULL.
+ *   r may be x (in place).  No other buffers overlap.
+ * Errors the host sees: PA_ERR_NULL, PA_ERR_SHAPE (sizes), PA_ERR_ALIGN, PA_ERR_SCALE (residual_scale or eps
+ * not finite, eps < 0), PA_ERR_MODE, PA_ERR_NOT_DEVICE.  Bad cu_seqlens: PA_ERR_CU_SEQLENS in the status word.
+ * Bitwise deterministic.
+ */
+PA_API int pa_block_norm_fwd(const pa_block_norm_desc* desc, const void* x, const void* y, void* r, void* z,
+                             void* stream);
+
+/*
+ * pa_block_norm_bwd -- enqueue the gradients of the join: from dr = dL/dr (the later uses of r; NULL counts
+ * as 0) and dz = dL/dz, with dr' = dr + the norm's gradient,
+ *     dx = residual_scale * dr',  dy = N_post's gradient of gate[s] * w_post * dr',
+ *     dgate[s] = sum over s's tokens of dr' u,  dscale[s] = sum of dz N_pre(r) w_pre,  dshift[s] = sum of dz,
+ *     dw_post = sum over all tokens of dr' gate N_post(y),  dw_pre = sum of dz (1 + scale) N_pre(r).
+ *   r            as the forward stored it (x when y is NULL).
+ *   dz           NULL exactly when pre is NONE; with dz NULL, dr is given.
+ *   dx           may be dr (in place).       dy   NULL exactly when y is.
+ *   dgate, dscale, dshift   fp32 [batch, hidden], NULL if not wanted; a segment without tokens gets 0.
+ *   dw_post, dw_pre         fp32 [hidden], NULL if not wanted.
+ *     A gradient of something that was not given (a NULL gate, ...) must be NULL: PA_ERR_MODE.
+ *   workspace    pa_block_norm_workspace_bytes(batch, total_tokens, hidden) bytes, 16-byte aligned; only read
+ *                (and may only be NULL if it is not) when one of the five sums is wanted.
+ * Column sums are added in a fixed order: bitwise deterministic.
+ */
+PA_API int64_t pa_block_norm_workspace_bytes(int32_t batch, int32_t total_tokens, int32_t hidden);
+PA_API int pa_block_norm_bwd(const pa_block_norm_desc* desc, const void* r, const void* y, const void* dr,
+                             const void* dz, void* dx, void* dy, float* dgate, float* dscale, float* dshift,
+                             float* dw_post, float* dw_pre, void* workspace, int64_t workspace_bytes, void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* PACKATTN_BLOCK_H_ */

@@ -1,0 +1,122 @@
+"""The entry points of packattn_block.h on a machine without a GPU: declared, exported, and refusing bad arguments
+before any CUDA call."""
+import ctypes
+import math
+import subprocess
+
+import pytest
+import torch
+
+import dit_resolution_packed_b200 as pa
+from dit_resolution_packed_b200 import _build, block
+
+
+@pytest.fixture(scope="module")
+def lib():
+    _build.build()
+    return pa.load_library()
+
+
+def test_header_and_exports(lib):
+    names = pa.header_functions(pa.BLOCK_HEADER_PATH)
+    assert "pa_block_norm_fwd" in names and len(names) == len(set(names))
+    out = subprocess.run(["nm", "-D", "--defined-only", pa.LIB_PATH], capture_output=True, text=True, check=True)
+    exported = {line.split()[-1] for line in out.stdout.splitlines() if " T " in line}
+    assert set(names) <= exported
+    assert exported <= set(names) | set(pa.header_functions()) | {"_init", "_fini"}
+    for name in names:
+        assert getattr(lib, name).argtypes is not None, f"{name} has no declared argument types"
+
+
+def test_status_strings():
+    texts = [pa.status_string(c) for c in (pa.PA_ERR_WORKSPACE, pa.PA_ERR_BLOCKS, pa.PA_ERR_MODE)]
+    assert len(set(texts)) == 3 and "unknown status" not in texts
+
+
+# ---------------------------------------------------------------- norms
+
+def _desc(**kw):
+    base = dict(total_tokens=4, batch=1, hidden=64, residual_fp32=0, param_fp32=0, post=0, pre=1, residual_scale=1.0,
+                eps=1e-6, cu_seqlens=4, gate=None, scale=None, shift=None, gate_stride=0, scale_stride=0,
+                shift_stride=0, w_post=None, w_pre=None)
+    base.update(kw)
+    return block.BlockNormDesc(**base)
+
+
+def _fwd(lib, x=16, y=None, r=None, z=16, **kw):
+    return lib.pa_block_norm_fwd(ctypes.byref(_desc(**kw)), x, y, r, z, None)
+
+
+def _bwd(lib, r=16, y=None, dr=16, dz=16, dx=16, dy=None, sums=(None,) * 5, ws=None, ws_bytes=0, **kw):
+    return lib.pa_block_norm_bwd(ctypes.byref(_desc(**kw)), r, y, dr, dz, dx, dy, *sums, ws, ws_bytes, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(hidden=60), pa.PA_ERR_SHAPE), (dict(hidden=0), pa.PA_ERR_SHAPE), (dict(hidden=8200), pa.PA_ERR_SHAPE),
+    (dict(total_tokens=-1), pa.PA_ERR_SHAPE), (dict(batch=-1), pa.PA_ERR_SHAPE), (dict(batch=0), pa.PA_ERR_SHAPE),
+    (dict(eps=math.nan), pa.PA_ERR_SCALE), (dict(eps=-1.0), pa.PA_ERR_SCALE),
+    (dict(y=16, r=16, residual_scale=math.inf), pa.PA_ERR_SCALE),
+    (dict(pre=3), pa.PA_ERR_MODE), (dict(post=-1), pa.PA_ERR_MODE), (dict(residual_fp32=2), pa.PA_ERR_MODE),
+    (dict(pre=0), pa.PA_ERR_MODE), (dict(z=None), pa.PA_ERR_MODE), (dict(pre=0, z=None), pa.PA_ERR_MODE),
+    (dict(pre=0, z=None, y=16, r=16, scale=16), pa.PA_ERR_MODE),
+    (dict(r=16), pa.PA_ERR_MODE), (dict(post=1), pa.PA_ERR_MODE), (dict(gate=16), pa.PA_ERR_MODE),
+    (dict(residual_scale=0.5), pa.PA_ERR_MODE), (dict(w_post=16), pa.PA_ERR_MODE),
+    (dict(x=None), pa.PA_ERR_NULL), (dict(y=16), pa.PA_ERR_NULL), (dict(scale=16, cu_seqlens=None), pa.PA_ERR_NULL),
+    (dict(x=8), pa.PA_ERR_ALIGN), (dict(z=24), pa.PA_ERR_ALIGN), (dict(scale=24), pa.PA_ERR_ALIGN),
+    (dict(scale=16, scale_stride=68), pa.PA_ERR_ALIGN), (dict(shift=16, shift_stride=-64), pa.PA_ERR_SHAPE),
+    (dict(w_pre=4), pa.PA_ERR_ALIGN), (dict(scale=16, cu_seqlens=6), pa.PA_ERR_ALIGN),
+    (dict(total_tokens=0), pa.PA_OK), (dict(total_tokens=0, batch=0), pa.PA_OK),
+])
+def test_norm_fwd_refusals(lib, kw, code):
+    assert _fwd(lib, **kw) == code
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(dz=None), pa.PA_ERR_MODE), (dict(pre=0), pa.PA_ERR_MODE), (dict(pre=0, dz=None, dr=None), pa.PA_ERR_MODE),
+    (dict(y=16), pa.PA_ERR_MODE), (dict(dy=16), pa.PA_ERR_MODE), (dict(r=None), pa.PA_ERR_NULL),
+    (dict(dx=None), pa.PA_ERR_NULL), (dict(dx=20), pa.PA_ERR_ALIGN),
+    (dict(sums=(16, None, None, None, None)), pa.PA_ERR_MODE),
+    (dict(sums=(None, None, None, None, 16)), pa.PA_ERR_MODE),
+    (dict(sums=(None, 16, None, None, None), scale=16), pa.PA_ERR_WORKSPACE),
+    (dict(sums=(None, 16, None, None, None), scale=16, ws=16, ws_bytes=64), pa.PA_ERR_WORKSPACE),
+    (dict(sums=(None, 16, None, None, None), scale=16, ws=8, ws_bytes=1 << 20), pa.PA_ERR_WORKSPACE),
+    (dict(sums=(None, 24, None, None, None), scale=16, ws=16, ws_bytes=1 << 20), pa.PA_ERR_ALIGN),
+    (dict(total_tokens=0), pa.PA_OK),
+])
+def test_norm_bwd_refusals(lib, kw, code):
+    assert _bwd(lib, **kw) == code
+
+
+def test_norm_null_desc_and_workspace(lib):
+    assert lib.pa_block_norm_fwd(None, 16, None, None, 16, None) == pa.PA_ERR_NULL
+    assert lib.pa_block_norm_bwd(None, *([16] * 11), 16, 0, None) == pa.PA_ERR_NULL
+    assert pa.pa_block_norm_workspace_bytes(-1, 4, 64) == -1
+    assert pa.pa_block_norm_workspace_bytes(1, 4, 65) == -1
+    # per chunk of rows and per image, three rows of channels, and two more per image
+    assert pa.pa_block_norm_workspace_bytes(2, 0, 64) == 4 * (2 * 3 + 2 * 2) * 64
+    assert pa.pa_block_norm_workspace_bytes(1, 2 ** 31 - 1, 8192) > 2 ** 40
+
+
+def test_norm_python_checks():
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    cu = torch.tensor([0, 4], dtype=torch.int32)
+    m = torch.zeros(1, 64, dtype=torch.bfloat16)
+    with pytest.raises(TypeError):
+        pa.block_norm_fwd(x.half(), cu)
+    with pytest.raises(TypeError):
+        pa.block_norm_fwd(x, cu, scale=m, shift=m.float())
+    with pytest.raises(TypeError):
+        pa.block_norm_fwd(x, cu.long(), scale=m)
+    with pytest.raises(ValueError):
+        pa.block_norm_fwd(x, None, scale=m)
+    with pytest.raises(ValueError):
+        pa.block_norm_fwd(x, cu, pre="batch")
+    with pytest.raises(ValueError):
+        pa.block_norm_fwd(x, cu, scale=m[:, :32])
+    with pytest.raises(ValueError):
+        pa.block_norm_fwd(torch.zeros(64, 4, dtype=torch.bfloat16).t(), cu)
+    with pytest.raises(ValueError):
+        pa.block_norm_fwd(x, cu, w_pre=m)
+    with pytest.raises(pa.PackAttnError) as e:
+        pa.block_norm_fwd(x, cu, residual_scale=0.5)
+    assert e.value.code == pa.PA_ERR_MODE

@@ -12,9 +12,10 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libpackattn.so")
-SOURCES = ["packattn.cu", "block_norm.cu"]
+SOURCES = ["packattn.cu", "block_norm.cu", "rope_axes.cu"]
 HEADERS = ["sm100_ptx.cuh", "schedule.cuh", "attn_fwd_sm100.cuh", "attn_fwd_fp8_sm100.cuh", "attn_bwd_sm100.cuh",
-           "gemm_sm100.cuh", "exp2_poly.cuh", "host.h", "block_norm_sm100.cuh"]
+           "gemm_sm100.cuh", "exp2_poly.cuh", "host.h", "block_norm_sm100.cuh",
+           "rope_axes_sm100.cuh"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 

@@ -22,14 +22,23 @@ class BlockNormDesc(ctypes.Structure):
                 ("shift_stride", ctypes.c_int64), ("w_post", ctypes.c_void_p), ("w_pre", ctypes.c_void_p)]
 
 
+class RopeAxesDesc(ctypes.Structure):
+    """``pa_rope_axes_desc``."""
+    _fields_ = [("axes", ctypes.c_int32), ("dims", ctypes.c_int32 * 4), ("theta", ctypes.c_double * 4),
+                ("interleaved", ctypes.c_int32)]
+
+
 def declare(lib):
     """Sets the argument types of the header's functions on a loaded library."""
     vp, i32, i64, f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
-    norm = ctypes.POINTER(BlockNormDesc)
+    norm, rope = ctypes.POINTER(BlockNormDesc), ctypes.POINTER(RopeAxesDesc)
     for name, res, args in (
             ("pa_block_norm_fwd", ctypes.c_int, [norm, vp, vp, vp, vp, vp]),
             ("pa_block_norm_workspace_bytes", i64, [i32, i32, i32]),
-            ("pa_block_norm_bwd", ctypes.c_int, [norm] + [vp] * 12 + [i64, vp])):
+            ("pa_block_norm_bwd", ctypes.c_int, [norm] + [vp] * 12 + [i64, vp]),
+            ("pa_rope_axes", ctypes.c_int, [vp, vp, vp, i32, i32, i32, rope, i32, vp, vp, vp]),
+            ("pa_rope_axes_workspace_bytes", i64, [i32, i32]),
+            ("pa_qkv_rope_axes_fwd", ctypes.c_int, [vp, vp, vp, i32, i32, i32, i32, rope, vp, vp, vp, vp, i64, vp])):
         fn = getattr(lib, name)
         fn.restype, fn.argtypes = res, args
 
@@ -188,3 +197,80 @@ def block_norm_bwd(r, cu_seqlens=None, dr=None, dz=None, *, y=None, gate=None, p
                            stream=stream)
     _raise_on(rc, "pa_block_norm_bwd")
     return out
+
+
+# ---------------------------------------------------------------- rotary positions with several axes
+
+def _rope_desc(pos, total, dims, theta, interleaved):
+    import torch
+    dims = [int(n) for n in dims]
+    bases = [float(theta)] * len(dims) if isinstance(theta, (int, float)) else [float(b) for b in theta]
+    if not 1 <= len(dims) <= 4 or len(bases) != len(dims):
+        raise ValueError("dims and theta: 1 to 4 axes, one base or one per axis")
+    _check(torch.float32, (total, len(dims)), pos=pos)
+    desc = RopeAxesDesc(axes=len(dims), interleaved=int(bool(interleaved)))
+    for a, (n, b) in enumerate(zip(dims, bases)):
+        desc.dims[a], desc.theta[a] = n, b
+    return desc
+
+
+def pa_rope_axes(q, k, pos, dims, theta, interleaved, inverse, q_out, k_out, stream=None):
+    """C ``pa_rope_axes``: q, k (or None), q_out, k_out bf16 [T, H, d], pos fp32 [T, axes].  Returns the status."""
+    import torch
+    if q.dim() != 3:
+        raise ValueError("q must be [T, H, d]")
+    _check(torch.bfloat16, q.shape, q=q, k=k, q_out=q_out, k_out=k_out)
+    T, H, d = q.shape
+    desc = _rope_desc(pos, T, dims, theta, interleaved)
+    return _library().pa_rope_axes(_p(q), _p(k), _p(pos), T, H, d, ctypes.byref(desc), int(bool(inverse)), _p(q_out),
+                                   _p(k_out), _handle(stream, q))
+
+
+def _rope_axes(q, k, pos, dims, theta, interleaved, inverse, stream):
+    import torch
+    with _under(stream):
+        q_out = torch.empty_like(q)
+        k_out = torch.empty_like(k) if k is not None else None
+    _raise_on(pa_rope_axes(q, k, pos, dims, theta, interleaved, inverse, q_out, k_out, stream), "pa_rope_axes")
+    return q_out, k_out
+
+
+def rope_axes_fwd(q, k, pos, dims, theta=10000.0, interleaved=False, stream=None):
+    """q and k [T, H, d] turned by positions with several axes: pos fp32 [T, axes]; dims, the channels of each axis
+    (their sum at most d, the channels behind them stay); theta one base or one per axis.  k may be None."""
+    return _rope_axes(q, k, pos, dims, theta, interleaved, False, stream)
+
+
+def rope_axes_bwd(dq, dk, pos, dims, theta=10000.0, interleaved=False, stream=None):
+    """Gradients of ``rope_axes_fwd``'s inputs from those of its outputs: the inverse rotation."""
+    return _rope_axes(dq, dk, pos, dims, theta, interleaved, True, stream)
+
+
+def pa_rope_axes_workspace_bytes(total_tokens, head_dim):
+    """C ``pa_rope_axes_workspace_bytes``."""
+    return int(_library().pa_rope_axes_workspace_bytes(int(total_tokens), int(head_dim)))
+
+
+def pa_qkv_rope_axes_fwd(x, w_qkv, pos, dims, theta, interleaved, q, k, v, workspace, stream=None):
+    """C ``pa_qkv_rope_axes_fwd``: x [T, C], w_qkv [3*H*d, C], q, k, v [T, H, d] (bf16), workspace a byte tensor."""
+    import torch
+    T, C = x.shape
+    _, H, d = q.shape
+    _check(torch.bfloat16, (T, C), x=x)
+    _check(torch.bfloat16, (3 * H * d, C), w_qkv=w_qkv)
+    _check(torch.bfloat16, (T, H, d), q=q, k=k, v=v)
+    desc = _rope_desc(pos, T, dims, theta, interleaved)
+    return _library().pa_qkv_rope_axes_fwd(_p(x), _p(w_qkv), _p(pos), T, C, H, d, ctypes.byref(desc), _p(q), _p(k),
+                                           _p(v), _p(workspace), workspace.numel(), _handle(stream, x))
+
+
+def qkv_rope_axes_fwd(x, w_qkv, pos, heads, head_dim, dims, theta=10000.0, interleaved=False, stream=None):
+    """Fused QKV projection with ``rope_axes_fwd``'s rotation in its epilogue; returns q, k, v bf16 [T, H, d]."""
+    import torch
+    T = x.shape[0]
+    with _under(stream):
+        q, k, v = (torch.empty(T, heads, head_dim, dtype=torch.bfloat16, device=x.device) for _ in range(3))
+        ws = torch.empty(max(pa_rope_axes_workspace_bytes(T, head_dim), 0), dtype=torch.uint8, device=x.device)
+    _raise_on(pa_qkv_rope_axes_fwd(x, w_qkv, pos, dims, theta, interleaved, q, k, v, ws, stream),
+              "pa_qkv_rope_axes_fwd")
+    return q, k, v

@@ -16,8 +16,6 @@
 // them does, so no two meet in a slot.  A second kernel adds the slots of a segment in order, a third one
 // forms dw_post and dw_pre from the per-segment sums (sum_t dr' gate yhat = sum_s gate[s] sum_{t in s} dr' yhat).
 #pragma once
-#include <cuda_bf16.h>
-
 #include <cstdint>
 
 #include "sm100_ptx.cuh"
@@ -50,19 +48,6 @@ struct NormParams {
   int32_t* status;
   int32_t err_cu;
 };
-
-__device__ __forceinline__ void bf16x8_to_f32(const uint4& a, float (&v)[8]) {
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
-}
-__device__ __forceinline__ uint4 f32_to_bf16x8(const float (&v)[8]) {
-  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                    pack_bf16x2(v[6], v[7]));
-}
 
 // Eight channels as they lie in memory, held between their load and their use.
 template <bool kF32>

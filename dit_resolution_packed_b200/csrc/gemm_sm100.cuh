@@ -32,7 +32,9 @@ constexpr int kGemmStageBytes = kGemmABytes + kGemmBBytes;
 constexpr int kGemmOffBar = kGemmStages * kGemmStageBytes;
 constexpr int kGemmSmemBytes = kGemmOffBar + 256 + 1024;  // + 1024 for base alignment
 
-enum GemmEpilogue : int { kEpiPlain = 0, kEpiQkvRope = 1 };
+// kEpiQkvAxes: the QKV epilogue with a table row per token (positions with several axes) instead of a row per
+// position, and pairs in halves or interleaved.
+enum GemmEpilogue : int { kEpiPlain = 0, kEpiQkvRope = 1, kEpiQkvAxes = 2 };
 
 // Tile order: bands of kGemmGroupM row tiles, each band walked N tile by N tile, so the
 // tiles running at once share a few x rows and about half of W's panels.  Measured on
@@ -63,6 +65,7 @@ struct GemmParams {
   int32_t heads, head_dim;
   const int32_t* pos;    // QKV: position of every token inside its segment
   const float2* rope;    // QKV: (cos, sin) [rope_rows][d/2], nullptr = no rotation
+  int32_t interleaved;   // axes: pair p is channels (2p, 2p + 1) instead of (p, p + d/2)
   int32_t* status;
   uint64_t wait_limit_ns;
   int32_t err_timeout;
@@ -173,6 +176,20 @@ __device__ __forceinline__ void rope32(uint32_t (&lo)[32], uint32_t (&hi)[32], c
   }
 }
 
+// The same of 16 interleaved pairs (x_2p, x_2p+1): 32 neighbouring channels.
+__device__ __forceinline__ void rope32_interleaved(uint32_t (&x)[32], const float2* cs) {
+#pragma unroll
+  for (int i = 0; i < 16; i += 2) {
+    const float4 t = *reinterpret_cast<const float4*>(cs + i);
+    const float a0 = __uint_as_float(x[2 * i]), b0 = __uint_as_float(x[2 * i + 1]);
+    const float a1 = __uint_as_float(x[2 * i + 2]), b1 = __uint_as_float(x[2 * i + 3]);
+    x[2 * i] = __float_as_uint(a0 * t.x - b0 * t.y);
+    x[2 * i + 1] = __float_as_uint(a0 * t.y + b0 * t.x);
+    x[2 * i + 2] = __float_as_uint(a1 * t.z - b1 * t.w);
+    x[2 * i + 3] = __float_as_uint(a1 * t.w + b1 * t.z);
+  }
+}
+
 // 32 fp32 values -> bf16 -> four 16-byte stores at dst.
 __device__ __forceinline__ void store32_bf16(uint16_t* dst, const uint32_t (&v)[32]) {
   uint4* d4 = reinterpret_cast<uint4*>(dst);
@@ -222,7 +239,8 @@ __device__ __forceinline__ void gemm_epilogue(const GemmParams& p, GemmBars* bar
     } else {
       const int d = p.head_dim, hd = p.heads * p.head_dim;
       const int half = d >> 1;
-      const int prow = (row_ok && p.rope != nullptr) ? __ldg(p.pos + row) : 0;  // no positions without RoPE
+      // row of the table: the token itself, or its position (none without RoPE)
+      const int prow = kEpi == kEpiQkvAxes ? row : (row_ok && p.rope != nullptr) ? __ldg(p.pos + row) : 0;
       // the tile holds 256 / d whole heads (d in {64, 128}, n0 a multiple of 256, and the
       // q / k / v boundaries are multiples of d)
       const int heads_in_tile = kGemmBN / d;
@@ -242,7 +260,13 @@ __device__ __forceinline__ void gemm_epilogue(const GemmParams& p, GemmBars* bar
           PA_TMEM_LD32(tacc + c_head0 + half + c0, hi);
           tmem_wait_ld();
           if (row_ok) {
-            if (rotate) rope32(lo, hi, p.rope + static_cast<size_t>(prow) * half + c0);
+            const float2* cs = p.rope + static_cast<size_t>(prow) * half;
+            if (kEpi == kEpiQkvAxes && rotate && p.interleaved) {
+              rope32_interleaved(lo, cs + c0 / 2);
+              rope32_interleaved(hi, cs + (half + c0) / 2);
+            } else if (rotate) {
+              rope32(lo, hi, cs + c0);
+            }
             store32_bf16(dst + c0, lo);
             store32_bf16(dst + half + c0, hi);
           }

@@ -8,6 +8,8 @@
 #include <cstdint>
 #include <initializer_list>
 
+struct pa_rope_axes_desc;
+
 namespace pa {
 namespace host {
 
@@ -39,6 +41,12 @@ class Call {
 bool encode_rows(CUtensorMap* m, const void* base, int32_t rows, int32_t heads, int32_t head_dim);
 // Tensor map of a bf16 row-major [outer, inner] matrix, box {64, box_outer}, 128-byte swizzle.
 bool encode_matrix(CUtensorMap* m, const void* base, int64_t inner, int64_t outer, uint32_t box_outer);
+
+// Positions with several axes (rope_axes.cu): PA_OK or why a description is refused; the (cos, sin) of every
+// token and pair into `table`.
+int check_rope_axes(const pa_rope_axes_desc* rope, int32_t head_dim);
+int launch_rope_table(const float* pos, int32_t total, int32_t head_dim, const pa_rope_axes_desc* rope, void* table,
+                      cudaStream_t stream);
 
 inline int launch_status() { return cudaGetLastError() == cudaSuccess ? 0 : -8; }
 

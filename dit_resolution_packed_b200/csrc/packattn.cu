@@ -171,6 +171,9 @@ int ensure_device(int device) {
   if (cudaFuncSetAttribute(pa::gemm_kernel<pa::kEpiQkvRope>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            pa::kGemmSmemBytes) != cudaSuccess)
     return PA_ERR_CUDA;
+  if (cudaFuncSetAttribute(pa::gemm_kernel<pa::kEpiQkvAxes>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           pa::kGemmSmemBytes) != cudaSuccess)
+    return PA_ERR_CUDA;
   if (cudaFuncSetAttribute(pa::attn_bwd_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            pa::BwdCfg<64>::kSmemBytes) != cudaSuccess)
     return PA_ERR_CUDA;
@@ -722,6 +725,48 @@ int pa_qkv_rope_fwd(const void* x, const void* w_qkv, const int32_t* cu_seqlens,
   gp.wait_limit_ns = static_cast<uint64_t>(g_wait_limit_ms) * 1000000ull;
   gp.err_timeout = PA_ERR_TIMEOUT;
   return launch_gemm<pa::kEpiQkvRope>(gp, dev, stream);
+}
+
+int pa_qkv_rope_axes_fwd(const void* x, const void* w_qkv, const float* pos, int32_t total_tokens, int32_t hidden,
+                         int32_t heads, int32_t head_dim, const pa_rope_axes_desc* rope, void* q, void* k, void* v,
+                         void* workspace, int64_t workspace_bytes, void* stream_handle) {
+  if (head_dim != 64 && head_dim != 128) return PA_ERR_HEAD_DIM;
+  if (heads < 1 || total_tokens < 0 || hidden < 1 || hidden % 8 != 0 ||
+      static_cast<int64_t>(heads) * head_dim * 3 >= (int64_t(1) << 30))
+    return PA_ERR_SHAPE;
+  int rc = pa::host::check_rope_axes(rope, head_dim);
+  if (rc != PA_OK || total_tokens == 0) return rc;
+  if (!x || !w_qkv || !pos || !q || !k || !v) return PA_ERR_NULL;
+  const void* a16[5] = {x, w_qkv, q, k, v};
+  for (const void* ptr : a16)
+    if (!aligned(ptr, 16)) return PA_ERR_ALIGN;
+  if (!aligned(pos, 4)) return PA_ERR_ALIGN;
+  if (!workspace || !aligned(workspace, 16) || workspace_bytes < pa_rope_axes_workspace_bytes(total_tokens, head_dim))
+    return PA_ERR_WORKSPACE;
+  int dev = -1;
+  if ((rc = pa::host::common_device({x, w_qkv, pos, q, k, v, workspace}, &dev)) != PA_OK) return rc;
+  pa::host::Call call(dev, stream_handle);
+  if (call.rc != PA_OK) return call.rc;
+  if ((rc = pa::host::launch_rope_table(pos, total_tokens, head_dim, rope, workspace, call.stream)) != PA_OK) return rc;
+  pa::GemmParams gp;
+  std::memset(&gp, 0, sizeof(gp));
+  const int32_t N = 3 * heads * head_dim;
+  if (!encode_2d(&gp.tm_a, x, hidden, total_tokens, 128) || !encode_2d(&gp.tm_b, w_qkv, hidden, N, 256))
+    return PA_ERR_CUDA;
+  gp.M = total_tokens;
+  gp.N = N;
+  gp.K = hidden;
+  gp.q = q;
+  gp.k = k;
+  gp.v = v;
+  gp.heads = heads;
+  gp.head_dim = head_dim;
+  gp.rope = static_cast<const float2*>(workspace);
+  gp.interleaved = rope->interleaved;
+  gp.status = call.status;
+  gp.wait_limit_ns = call.wait_limit_ns;
+  gp.err_timeout = PA_ERR_TIMEOUT;
+  return launch_gemm<pa::kEpiQkvAxes>(gp, dev, call.stream);
 }
 
 int pa_get_error(void* stream_handle) {

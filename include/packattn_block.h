@@ -4,6 +4,8 @@
  *
  *   pa_block_norm_fwd / _bwd         gated residual join with the norm behind a block and the norm in
  *                                    front of the next
+ *   pa_rope_axes / pa_qkv_rope_axes_fwd
+ *                                    rotary positions with several axes (time, height, width)
  *
  * Unlike packattn.h's entry points these take their scratch memory from the caller, so that two captured
  * graphs, or two streams, that use different buffers never share one; the library itself holds only the
@@ -98,6 +100,44 @@ PA_API int64_t pa_block_norm_workspace_bytes(int32_t batch, int32_t total_tokens
 PA_API int pa_block_norm_bwd(const pa_block_norm_desc* desc, const void* r, const void* y, const void* dr,
                              const void* dz, void* dx, void* dy, float* dgate, float* dscale, float* dshift,
                              float* dw_post, float* dw_pre, void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * Rotary positions with several axes.  The d/2 rotated pairs of a head are shared out over the axes:
+ * axis a has dims[a] channels, that is dims[a]/2 pairs, in order; pair i of axis a turns by the angle
+ *     pos[t, a] * theta[a]^(-2 i / dims[a]).
+ * Pair p of the head is (x_p, x_{p + d/2}), or (x_{2p}, x_{2p+1}) when interleaved; pairs past the axes' total
+ * (sum of dims < head_dim) are left as they are.  Angles are formed and reduced in fp64.
+ *
+ *   axes        1 .. 4;  dims, theta: host arrays of that length; dims even, >= 2, sum <= head_dim; theta > 0.
+ *   pos         device, fp32, [total_tokens, axes], contiguous, 4-byte aligned (any position, fractions too).
+ *   interleaved 0 or 1.
+ */
+typedef struct pa_rope_axes_desc {
+  int32_t axes;
+  int32_t dims[4];
+  double theta[4];
+  int32_t interleaved;
+} pa_rope_axes_desc;
+
+/*
+ * pa_rope_axes -- rotate q and k [total_tokens, heads, head_dim] (bf16, contiguous, 16-byte aligned) on `stream`.
+ *   inverse     0: the rotation; 1: its inverse, which is also its gradient (dq, dk in, gradients out).
+ *   q_out, k_out may be q and k (in place); each rounded once.  k and k_out may both be NULL (q alone).
+ */
+PA_API int pa_rope_axes(const void* q, const void* k, const float* pos, int32_t total_tokens, int32_t heads,
+                        int32_t head_dim, const pa_rope_axes_desc* rope, int32_t inverse, void* q_out, void* k_out,
+                        void* stream);
+
+/*
+ * pa_qkv_rope_axes_fwd -- pa_qkv_rope_fwd's projection with these positions: qkv = x W_qkv^T, q and k rotated
+ * in the GEMM's epilogue (fp32 accumulators), q, k, v rounded once.  Arguments as there.
+ *   workspace   pa_rope_axes_workspace_bytes(total_tokens, head_dim) bytes, 16-byte aligned: the (cos, sin) of
+ *               every token and pair.
+ */
+PA_API int64_t pa_rope_axes_workspace_bytes(int32_t total_tokens, int32_t head_dim);
+PA_API int pa_qkv_rope_axes_fwd(const void* x, const void* w_qkv, const float* pos, int32_t total_tokens,
+                                int32_t hidden, int32_t heads, int32_t head_dim, const pa_rope_axes_desc* rope,
+                                void* q, void* k, void* v, void* workspace, int64_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

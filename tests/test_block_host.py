@@ -120,3 +120,63 @@ def test_norm_python_checks():
     with pytest.raises(pa.PackAttnError) as e:
         pa.block_norm_fwd(x, cu, residual_scale=0.5)
     assert e.value.code == pa.PA_ERR_MODE
+
+
+# ---------------------------------------------------------------- rotary positions with several axes
+
+def _axes(dims=(32, 32), theta=(100.0, 100.0), inter=0, axes=None):
+    d = block.RopeAxesDesc(axes=len(dims) if axes is None else axes, interleaved=inter)
+    for i, (n, b) in enumerate(zip(dims, theta)):
+        d.dims[i], d.theta[i] = n, b
+    return ctypes.byref(d)
+
+
+def _rope(lib, q=16, k=16, pos=16, total=4, heads=2, d=64, desc=None, inverse=0, qo=16, ko=16):
+    return lib.pa_rope_axes(q, k, pos, total, heads, d, _axes() if desc is None else desc, inverse, qo, ko, None)
+
+
+def _qkv(lib, x=16, w=16, pos=16, total=4, hidden=64, heads=2, d=64, desc=None, q=16, k=16, v=16, ws=16,
+         ws_bytes=1 << 20):
+    return lib.pa_qkv_rope_axes_fwd(x, w, pos, total, hidden, heads, d, _axes() if desc is None else desc, q, k, v, ws,
+                                    ws_bytes, None)
+
+
+def test_rope_refusals(lib):
+    for call in (_rope, _qkv):
+        assert call(lib, d=96) == pa.PA_ERR_HEAD_DIM
+        assert call(lib, heads=0) == pa.PA_ERR_SHAPE
+        assert call(lib, total=-1) == pa.PA_ERR_SHAPE
+        assert call(lib, total=0) == pa.PA_OK
+        assert call(lib, desc=_axes(dims=(31, 32))) == pa.PA_ERR_SHAPE
+        assert call(lib, desc=_axes(dims=(0, 32))) == pa.PA_ERR_SHAPE
+        assert call(lib, desc=_axes(dims=(-2, 32))) == pa.PA_ERR_SHAPE
+        assert call(lib, desc=_axes(dims=(34, 32))) == pa.PA_ERR_SHAPE
+        assert call(lib, desc=_axes(axes=0)) == pa.PA_ERR_SHAPE
+        assert call(lib, desc=_axes(axes=5)) == pa.PA_ERR_SHAPE
+        assert call(lib, desc=_axes(inter=2)) == pa.PA_ERR_SHAPE
+        assert call(lib, desc=_axes(theta=(0.0, 1.0))) == pa.PA_ERR_SCALE
+        assert call(lib, desc=_axes(theta=(math.inf, 1.0))) == pa.PA_ERR_SCALE
+        assert call(lib, pos=None) == pa.PA_ERR_NULL
+        assert call(lib, pos=18) == pa.PA_ERR_ALIGN
+        assert call(lib, q=8) == pa.PA_ERR_ALIGN
+        assert call(lib, k=None) == pa.PA_ERR_NULL
+    assert lib.pa_rope_axes(16, 16, 16, 4, 2, 64, None, 0, 16, 16, None) == pa.PA_ERR_NULL
+    assert _rope(lib, inverse=2) == pa.PA_ERR_SHAPE
+    assert _rope(lib, qo=None) == pa.PA_ERR_NULL
+    assert _rope(lib, heads=1 << 20) == pa.PA_ERR_SHAPE
+    assert _qkv(lib, hidden=12) == pa.PA_ERR_SHAPE
+    assert _qkv(lib, ws=None) == pa.PA_ERR_WORKSPACE
+    assert _qkv(lib, ws_bytes=4 * 32 * 8 - 1) == pa.PA_ERR_WORKSPACE
+    assert pa.pa_rope_axes_workspace_bytes(4, 64) == 4 * 32 * 8
+    assert pa.pa_rope_axes_workspace_bytes(-1, 64) == -1 and pa.pa_rope_axes_workspace_bytes(4, 80) == -1
+    q, pos = torch.zeros(4, 2, 64, dtype=torch.bfloat16), torch.zeros(4, 2)
+    with pytest.raises(ValueError):
+        pa.rope_axes_fwd(q, q, pos, [16, 16, 16])
+    with pytest.raises(ValueError):
+        pa.rope_axes_fwd(q, q, pos, [32, 32], [1.0])
+    with pytest.raises(ValueError):
+        pa.rope_axes_fwd(q, q, pos[:3], [32, 32])
+    with pytest.raises(TypeError):
+        pa.rope_axes_fwd(q, q, pos.double(), [32, 32])
+    with pytest.raises(TypeError):
+        pa.rope_axes_fwd(q, q.float(), pos, [32, 32])

@@ -454,5 +454,7 @@ def pa_profile_read():
 
 # the block around the attention and its sparse form (include/packattn_block.h)
 from .block import (  # noqa: E402
-    block_norm_bwd, block_norm_fwd, pa_block_norm_bwd, pa_block_norm_fwd, pa_block_norm_workspace_bytes,
-    pa_qkv_rope_axes_fwd, pa_rope_axes, pa_rope_axes_workspace_bytes, qkv_rope_axes_fwd, rope_axes_bwd, rope_axes_fwd)
+    block_norm_bwd, block_norm_fwd, block_select, block_sparse_attn_bwd, block_sparse_attn_fwd, pa_block_norm_bwd,
+    pa_block_norm_fwd, pa_block_norm_workspace_bytes, pa_block_rows, pa_block_select, pa_block_select_workspace_bytes,
+    pa_block_sparse_attn_bwd, pa_block_sparse_attn_fwd, pa_block_sparse_workspace_bytes, pa_qkv_rope_axes_fwd,
+    pa_rope_axes, pa_rope_axes_workspace_bytes, qkv_rope_axes_fwd, rope_axes_bwd, rope_axes_fwd)

@@ -12,10 +12,10 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libpackattn.so")
-SOURCES = ["packattn.cu", "block_norm.cu", "rope_axes.cu"]
+SOURCES = ["packattn.cu", "block_norm.cu", "rope_axes.cu", "sparse.cu"]
 HEADERS = ["sm100_ptx.cuh", "schedule.cuh", "attn_fwd_sm100.cuh", "attn_fwd_fp8_sm100.cuh", "attn_bwd_sm100.cuh",
            "gemm_sm100.cuh", "exp2_poly.cuh", "host.h", "block_norm_sm100.cuh",
-           "rope_axes_sm100.cuh"]
+           "rope_axes_sm100.cuh", "sparse_plan_sm100.cuh", "attn_sparse_fwd_sm100.cuh"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
@@ -53,7 +53,8 @@ def _check_registers(ptxas_log):
             kernel = m.group(1)
             continue
         m = re.search(r"Used (\d+) registers", line)
-        if m and kernel and any(n in kernel for n in ("attn_fwd_kernel", "attn_fwd_fp8_kernel", "attn_bwd_kernel")):
+        if m and kernel and any(
+                n in kernel for n in ("attn_fwd_kernel", "attn_fwd_fp8_kernel", "attn_sparse_fwd_kernel", "attn_bwd_kernel")):
             regs = int(m.group(1))
             if "attn_bwd_kernel" in kernel:
                 if regs > BWD_MAX_REGS:

@@ -8,6 +8,7 @@ they may be freed or captured into a graph like any other tensor of that stream.
 import contextlib
 import ctypes
 import math
+import math
 
 NORM_KINDS = {"none": 0, "layer": 1, "rms": 2}
 
@@ -38,7 +39,15 @@ def declare(lib):
             ("pa_block_norm_bwd", ctypes.c_int, [norm] + [vp] * 12 + [i64, vp]),
             ("pa_rope_axes", ctypes.c_int, [vp, vp, vp, i32, i32, i32, rope, i32, vp, vp, vp]),
             ("pa_rope_axes_workspace_bytes", i64, [i32, i32]),
-            ("pa_qkv_rope_axes_fwd", ctypes.c_int, [vp, vp, vp, i32, i32, i32, i32, rope, vp, vp, vp, vp, i64, vp])):
+            ("pa_qkv_rope_axes_fwd", ctypes.c_int, [vp, vp, vp, i32, i32, i32, i32, rope, vp, vp, vp, vp, i64, vp]),
+            ("pa_block_rows", i64, [i32, i32]),
+            ("pa_block_select_workspace_bytes", i64, [i32, i32, i32, i32]),
+            ("pa_block_select", ctypes.c_int, [vp, vp, vp, i32, i32, i32, i32, i32, ctypes.c_double, i32, i32, vp, vp, vp,
+                                               i64, vp]),
+            ("pa_block_sparse_workspace_bytes", i64, [i32] * 7),
+            ("pa_block_sparse_attn_fwd", ctypes.c_int, [vp] * 4 + [i32] * 5 + [vp, vp, i32, f32, vp, vp, vp, i64, vp]),
+            ("pa_block_sparse_attn_bwd", ctypes.c_int, [vp] * 7 + [i32] * 5 + [vp, vp, i32, f32, vp, vp, vp, vp, i64,
+                                                                               vp])):
         fn = getattr(lib, name)
         fn.restype, fn.argtypes = res, args
 
@@ -274,3 +283,133 @@ def qkv_rope_axes_fwd(x, w_qkv, pos, heads, head_dim, dims, theta=10000.0, inter
     _raise_on(pa_qkv_rope_axes_fwd(x, w_qkv, pos, dims, theta, interleaved, q, k, v, ws, stream),
               "pa_qkv_rope_axes_fwd")
     return q, k, v
+
+
+# ---------------------------------------------------------------- attention over selected blocks
+
+BLOCK_TOKENS = 128
+
+
+def pa_block_rows(batch, total_tokens):
+    """C ``pa_block_rows``: rows of the block tables of a pack."""
+    return int(_library().pa_block_rows(int(batch), int(total_tokens)))
+
+
+def _pack(cu_seqlens, **tensors):
+    """Checks [T, H, d] bf16 tensors of one pack; returns T, H, d, B."""
+    import torch
+    _check(torch.int32, None, cu_seqlens=cu_seqlens)
+    first = next(iter(tensors.values()))
+    if first.dim() != 3:
+        raise ValueError("q, k and v must be [T, H, d]")
+    _check(torch.bfloat16, first.shape, **tensors)
+    return tuple(first.shape) + (cu_seqlens.numel() - 1,)
+
+
+def _lists(idx, cnt, heads, rows):
+    import torch
+    if idx.dim() != 3:
+        raise ValueError("idx must be [H, rows, width]")
+    _check(torch.int32, (heads, rows, idx.shape[2]), idx=idx)
+    _check(torch.int32, (heads, rows), cnt=cnt)
+    return idx.shape[2]
+
+
+def pa_block_select_workspace_bytes(batch, total_tokens, heads, head_dim):
+    """C ``pa_block_select_workspace_bytes``."""
+    return int(_library().pa_block_select_workspace_bytes(int(batch), int(total_tokens), int(heads), int(head_dim)))
+
+
+def pa_block_select(q, k, cu_seqlens, max_seqlen, density, min_blocks, idx, cnt, workspace, stream=None):
+    """C ``pa_block_select``: q, k bf16 [T, H, d]; idx int32 [H, rows, width], cnt int32 [H, rows] (written);
+    workspace a byte tensor.  Returns the status code."""
+    T, H, d, B = _pack(cu_seqlens, q=q, k=k)
+    width = _lists(idx, cnt, H, pa_block_rows(B, T))
+    return _library().pa_block_select(_p(q), _p(k), _p(cu_seqlens), B, T, H, d, int(max_seqlen), float(density),
+                                      int(min_blocks), width, _p(idx), _p(cnt), _p(workspace), workspace.numel(),
+                                      _handle(stream, q))
+
+
+def block_select(q, k, cu_seqlens, max_seqlen, density, min_blocks=1, stream=None):
+    """The key blocks that each block of 128 queries of an image attends to: of the image's nb blocks the
+    min(nb, max(min_blocks, ceil(density nb))) whose mean key has the largest product with the mean query.
+
+    Returns idx int32 [H, rows, width] (increasing, -1 behind the list) and cnt int32 [H, rows]; block b of image s
+    is row cu_seqlens[s] // 128 + s + b."""
+    import torch
+    T, H, d, B = _pack(cu_seqlens, q=q, k=k)
+    nb = max(1, -(-int(max_seqlen) // BLOCK_TOKENS))
+    width = min(nb, max(int(min_blocks), math.ceil(density * nb)))
+    with _under(stream):
+        idx = torch.empty(H, pa_block_rows(B, T), max(width, 1), dtype=torch.int32, device=q.device)
+        cnt = torch.empty(H, pa_block_rows(B, T), dtype=torch.int32, device=q.device)
+        ws = torch.empty(max(pa_block_select_workspace_bytes(B, T, H, d), 0), dtype=torch.uint8, device=q.device)
+    _raise_on(pa_block_select(q, k, cu_seqlens, max_seqlen, density, min_blocks, idx, cnt, ws, stream),
+              "pa_block_select")
+    return idx, cnt
+
+
+def pa_block_sparse_workspace_bytes(batch, total_tokens, heads, head_dim, max_seqlen, width, backward):
+    """C ``pa_block_sparse_workspace_bytes``."""
+    return int(_library().pa_block_sparse_workspace_bytes(int(batch), int(total_tokens), int(heads), int(head_dim),
+                                                          int(max_seqlen), int(width), int(bool(backward))))
+
+
+def pa_block_sparse_attn_fwd(q, k, v, cu_seqlens, max_seqlen, idx, cnt, scale, out, lse, workspace, stream=None):
+    """C ``pa_block_sparse_attn_fwd``: q, k, v, out bf16 [T, H, d], lse fp32 [T, H], idx int32 [H, rows, width], cnt
+    int32 [H, rows], workspace a byte tensor.  Returns the status code."""
+    import torch
+    T, H, d, B = _pack(cu_seqlens, q=q, k=k, v=v, out=out)
+    _check(torch.float32, (T, H), lse=lse)
+    width = _lists(idx, cnt, H, pa_block_rows(B, T))
+    return _library().pa_block_sparse_attn_fwd(_p(q), _p(k), _p(v), _p(cu_seqlens), B, T, H, d, int(max_seqlen),
+                                               _p(idx), _p(cnt), width, float(scale), _p(out), _p(lse), _p(workspace),
+                                               workspace.numel(), _handle(stream, q))
+
+
+def _sparse_workspace(q, cu_seqlens, max_seqlen, idx, backward):
+    import torch
+    T, H, d = q.shape
+    n = pa_block_sparse_workspace_bytes(cu_seqlens.numel() - 1, T, H, d, max(int(max_seqlen), 0), idx.shape[2], backward)
+    return torch.empty(max(n, 0), dtype=torch.uint8, device=q.device)
+
+
+def block_sparse_attn_fwd(q, k, v, cu_seqlens, max_seqlen, idx, cnt, scale=None, stream=None):
+    """``varlen_attn_fwd`` over the key blocks that idx and cnt list (from ``block_select``, or a pattern of the
+    caller's).  A query block with an empty list gets out = 0, lse = -inf.  Returns out bf16 [T, H, d], lse [T, H]."""
+    import torch
+    if scale is None:
+        scale = q.shape[-1] ** -0.5
+    with _under(stream):
+        out = torch.empty_like(q)
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+        ws = _sparse_workspace(q, cu_seqlens, max_seqlen, idx, False)
+    _raise_on(pa_block_sparse_attn_fwd(q, k, v, cu_seqlens, max_seqlen, idx, cnt, scale, out, lse, ws, stream),
+              "pa_block_sparse_attn_fwd")
+    return out, lse
+
+
+def pa_block_sparse_attn_bwd(q, k, v, out, lse, dout, cu_seqlens, max_seqlen, idx, cnt, scale, dq, dk, dv, workspace,
+                             stream=None):
+    """C ``pa_block_sparse_attn_bwd``: tensors as for ``pa_varlen_attn_bwd``, lists and workspace as for
+    ``pa_block_sparse_attn_fwd`` (backward = 1).  Returns the status code."""
+    import torch
+    T, H, d, B = _pack(cu_seqlens, q=q, k=k, v=v, out=out, dout=dout, dq=dq, dk=dk, dv=dv)
+    _check(torch.float32, (T, H), lse=lse)
+    width = _lists(idx, cnt, H, pa_block_rows(B, T))
+    return _library().pa_block_sparse_attn_bwd(_p(q), _p(k), _p(v), _p(out), _p(lse), _p(dout), _p(cu_seqlens), B, T, H,
+                                               d, int(max_seqlen), _p(idx), _p(cnt), width, float(scale), _p(dq),
+                                               _p(dk), _p(dv), _p(workspace), workspace.numel(), _handle(stream, q))
+
+
+def block_sparse_attn_bwd(q, k, v, out, lse, dout, cu_seqlens, max_seqlen, idx, cnt, scale=None, stream=None):
+    """Gradients of ``block_sparse_attn_fwd`` (the lists are constants); returns dq, dk, dv, bf16 [T, H, d]."""
+    import torch
+    if scale is None:
+        scale = q.shape[-1] ** -0.5
+    with _under(stream):
+        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+        ws = _sparse_workspace(q, cu_seqlens, max_seqlen, idx, True)
+    _raise_on(pa_block_sparse_attn_bwd(q, k, v, out, lse, dout, cu_seqlens, max_seqlen, idx, cnt, scale, dq, dk, dv, ws,
+                                       stream), "pa_block_sparse_attn_bwd")
+    return dq, dk, dv

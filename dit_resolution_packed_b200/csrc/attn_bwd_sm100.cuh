@@ -36,6 +36,11 @@
 //   warps 10-11 idle
 //   warps 12-15 dQ partial -> fp32 reductions (one thread per query row); dK, dV
 //              epilogue at the end of the item (one thread per key row)
+//
+// With kSparse the same kernel is the backward of the attention over listed key blocks: an item is (segment, head,
+// key block) and walks only the query blocks that name it, marked as bits by the plan kernels (in increasing order,
+// so dK and dV sum in a fixed order).  Tiles then come through the segment's own tensor maps, which read zeros past
+// its end, and a key block that nobody names writes zeros.
 #pragma once
 #include <cuda.h>
 
@@ -99,7 +104,13 @@ struct BwdParams {
   float scale, scale_log2;
   uint64_t wait_limit_ns;
   int32_t err_timeout;
+  // kSparse
+  const int32_t* desc;    // [items][kBwdDescInts]: seg, beg, len, head, k0, query blocks
+  const uint32_t* bits;   // [items][words] query blocks that name the key block
+  int32_t words;
+  const uint8_t* maps;    // [B][4] tensor maps: q, k, v, dout
 };
+constexpr int kBwdDescInts = 12;
 
 struct BwdBars {
   uint64_t kv_full, kv_empty;
@@ -111,7 +122,7 @@ struct BwdBars {
   uint64_t stage_full[2], stage_empty[2];  // per warpgroup: its queries' -lse2, -D*scale staging
   uint64_t sched_full[2], sched_empty[2];
   uint64_t drain;
-  int32_t sched_item[2][8];  // seg, beg, len, head, k0, n query tiles, -, id; seg < 0 = done
+  int32_t sched_item[2][8];  // seg, beg, len, head, k0, n query tiles, row of bits, id; seg < 0 = done
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -119,6 +130,36 @@ static_assert(sizeof(BwdBars) <= 512, "backward barrier block");
 
 struct BwdItem {
   int32_t seg, beg, len, head, k0, nq, id;
+  int32_t row;  // kSparse: row of the query-block bits
+};
+
+// The query tiles of an item, in order: all of the segment's, or those whose bits are set.
+template <bool kSparse>
+struct BwdQueryWalk {
+  const uint32_t* word;
+  uint32_t left;
+  int32_t base;
+  __device__ __forceinline__ BwdQueryWalk(const BwdParams& p, const BwdItem& w) {
+    if (kSparse && w.nq > 0) {
+      word = p.bits + static_cast<int64_t>(w.row) * p.words;
+      left = __ldg(word);
+      base = 0;
+    }
+  }
+  // the i-th query tile (called for i = 0 .. nq - 1: as many bits are set)
+  __device__ __forceinline__ int32_t next(int32_t i) {
+    if constexpr (kSparse) {
+      while (left == 0) {
+        left = __ldg(++word);
+        base += 32;
+      }
+      const int32_t q = base + __ffs(static_cast<int>(left)) - 1;
+      left &= left - 1;
+      return q;
+    } else {
+      return i;
+    }
+  }
 };
 
 __device__ __forceinline__ BwdItem bwd_decode_item(int32_t item, const BwdParams& p, int32_t n_sorted) {
@@ -136,15 +177,31 @@ __device__ __forceinline__ BwdItem bwd_decode_item(int32_t item, const BwdParams
   w.head = local / w.nq;
   w.k0 = (local - w.head * w.nq) * 128;
   w.id = item;
+  w.row = 0;
+  return w;
+}
+
+// kSparse: the item in the plan's descriptors.
+__device__ __forceinline__ BwdItem bwd_listed_item(int32_t item, const BwdParams& p) {
+  BwdItem w;
+  w.row = __ldg(p.order + item);
+  const int32_t* d = p.desc + static_cast<int64_t>(w.row) * kBwdDescInts;
+  w.seg = __ldg(d);
+  w.beg = __ldg(d + 1);
+  w.len = __ldg(d + 2);
+  w.head = __ldg(d + 3);
+  w.k0 = __ldg(d + 4);
+  w.nq = __ldg(d + 5);
+  w.id = item;
   return w;
 }
 
 __device__ __forceinline__ void bwd_store_item(volatile int32_t* d, const BwdItem& w) {
-  d[0] = w.seg; d[1] = w.beg; d[2] = w.len; d[3] = w.head; d[4] = w.k0; d[5] = w.nq; d[7] = w.id;
+  d[0] = w.seg; d[1] = w.beg; d[2] = w.len; d[3] = w.head; d[4] = w.k0; d[5] = w.nq; d[6] = w.row; d[7] = w.id;
 }
 __device__ __forceinline__ BwdItem bwd_load_item(const volatile int32_t* d) {
   BwdItem w;
-  w.seg = d[0]; w.beg = d[1]; w.len = d[2]; w.head = d[3]; w.k0 = d[4]; w.nq = d[5]; w.id = d[7];
+  w.seg = d[0]; w.beg = d[1]; w.len = d[2]; w.head = d[3]; w.k0 = d[4]; w.nq = d[5]; w.row = d[6]; w.id = d[7];
   return w;
 }
 
@@ -168,7 +225,7 @@ __device__ __forceinline__ bool bwd_drain_wait(uint64_t* bar, uint32_t parity, u
 }
 
 // ------------------------------------------------------------------ producer
-template <int D>
+template <int D, bool kSparse>
 __device__ __forceinline__ void bwd_producer(const BwdParams& p, uint8_t* smem, BwdBars* bars, const WaitCtl& wc,
                                              int32_t n_items, int32_t n_sorted) {
   using C = BwdCfg<D>;
@@ -186,14 +243,27 @@ __device__ __forceinline__ void bwd_producer(const BwdParams& p, uint8_t* smem, 
     const int32_t item = atomicAdd(p.next_item, 1);
     BwdItem w;
     if (item < n_items) {
-      w = bwd_decode_item(item, p, n_sorted);
+      w = kSparse ? bwd_listed_item(item, p) : bwd_decode_item(item, p, n_sorted);
     } else {
       w.seg = -1;
     }
     bwd_store_item(bars->sched_item[ss], w);
     mbar_arrive(&bars->sched_full[ss]);
     if (w.seg < 0) break;
+    if (kSparse && w.nq == 0) continue;
 
+    const uint8_t* maps = p.maps + (kSparse ? static_cast<size_t>(w.seg) * 4 * 128 : 0);
+    const void* mq = kSparse ? static_cast<const void*>(maps) : &p.tm_q;
+    const void* mk = kSparse ? static_cast<const void*>(maps + 128) : &p.tm_k;
+    const void* mv = kSparse ? static_cast<const void*>(maps + 256) : &p.tm_v;
+    const void* mdo = kSparse ? static_cast<const void*>(maps + 384) : &p.tm_do;
+    if (kSparse) {
+      fence_tmap_acquire(mq);
+      fence_tmap_acquire(mk);
+      fence_tmap_acquire(mv);
+      fence_tmap_acquire(mdo);
+    }
+    const int32_t row0 = kSparse ? 0 : w.beg;  // of the segment, in the maps' coordinates
     const int32_t xcol = w.head * D;
     if (!(ok = mbar_wait(&bars->kv_empty, (kv_round & 1u) ^ 1u, wc))) break;
     mbar_arrive_expect_tx(&bars->kv_full, 2u * C::kTileBytes);
@@ -202,20 +272,22 @@ __device__ __forceinline__ void bwd_producer(const BwdParams& p, uint8_t* smem, 
     ++kv_round;
 #pragma unroll
     for (int cb = 0; cb < C::kColBlocks; ++cb) {
-      tma_load_2d(smem + C::kOffK + cb * C::kBlockBytes, &p.tm_k, xcol + cb * 64, w.beg + w.k0, &bars->kv_full);
-      tma_load_2d(smem + C::kOffV + cb * C::kBlockBytes, &p.tm_v, xcol + cb * 64, w.beg + w.k0, &bars->kv_full);
+      tma_load_2d(smem + C::kOffK + cb * C::kBlockBytes, mk, xcol + cb * 64, row0 + w.k0, &bars->kv_full);
+      tma_load_2d(smem + C::kOffV + cb * C::kBlockBytes, mv, xcol + cb * 64, row0 + w.k0, &bars->kv_full);
     }
+    BwdQueryWalk<kSparse> walk(p, w);
     for (int32_t i = 0; ok && i < w.nq; ++i) {
+      const int32_t y = row0 + walk.next(i) * 128;
       if (!(ok = mbar_wait(&bars->qd_empty[qslot], qphase ^ 1u, wc))) break;
       mbar_arrive_expect_tx(&bars->qd_full[qslot], 2u * C::kTileBytes);
       q_armed |= 1u << qslot;
       q_armed_ph = (q_armed_ph & ~(1u << qslot)) | (qphase << qslot);
 #pragma unroll
       for (int cb = 0; cb < C::kColBlocks; ++cb) {
-        tma_load_2d(smem + C::kOffQ + qslot * C::kTileBytes + cb * C::kBlockBytes, &p.tm_q, xcol + cb * 64,
-                    w.beg + i * 128, &bars->qd_full[qslot]);
-        tma_load_2d(smem + C::kOffDO + qslot * C::kTileBytes + cb * C::kBlockBytes, &p.tm_do, xcol + cb * 64,
-                    w.beg + i * 128, &bars->qd_full[qslot]);
+        tma_load_2d(smem + C::kOffQ + qslot * C::kTileBytes + cb * C::kBlockBytes, mq, xcol + cb * 64, y,
+                    &bars->qd_full[qslot]);
+        tma_load_2d(smem + C::kOffDO + qslot * C::kTileBytes + cb * C::kBlockBytes, mdo, xcol + cb * 64, y,
+                    &bars->qd_full[qslot]);
       }
       if (++qslot == 2) {
         qslot = 0;
@@ -279,7 +351,7 @@ __device__ __forceinline__ void bwd_issue_dq(uint32_t issue, uint32_t d_tmem, ui
   }
 }
 
-template <int D>
+template <int D, bool kSparse>
 __device__ __forceinline__ void bwd_mma(const BwdParams& p, uint8_t* smem, BwdBars* bars, const WaitCtl& wc,
                                         uint32_t tmem) {
   using C = BwdCfg<D>;
@@ -298,6 +370,7 @@ __device__ __forceinline__ void bwd_mma(const BwdParams& p, uint8_t* smem, BwdBa
     if (got != -2 && leader) mbar_arrive(&bars->sched_empty[(sk - 1) & 1]);
     if (got == -2) ok = false;
     if (got <= 0) break;
+    if (kSparse && w.nq == 0) continue;
     if (!(ok = mbar_wait(&bars->kv_full, kv_round & 1u, wc))) break;
     ++kv_round;
     if (!(ok = mbar_wait(&bars->qd_full[qslot], qphase, wc))) break;
@@ -419,7 +492,7 @@ __device__ __forceinline__ void bwd_ew_units(uint32_t tA, uint32_t tB, const flo
 // every tile, one thread per key row, in units of 16 query columns (the loads of unit
 // u + 1 in flight while unit u is computed).  They go to tensor-memory columns
 // [64h, 64h + 32) of A and B: each warpgroup reads and writes only its own 64 columns.
-template <int D>
+template <int D, bool kSparse>
 __device__ __forceinline__ void bwd_elementwise(const BwdParams& p, uint8_t* smem, BwdBars* bars, const WaitCtl& wc,
                                                 uint32_t tmem, int h) {
   using C = BwdCfg<D>;
@@ -445,9 +518,11 @@ __device__ __forceinline__ void bwd_elementwise(const BwdParams& p, uint8_t* sme
     if (got <= 0) break;
     const bool key_ok = t < w.len - w.k0;
     bool ok = true;
+    BwdQueryWalk<kSparse> walk(p, w);
     for (int32_t i = 0; i < w.nq; ++i) {
+      const int32_t qi = walk.next(i);
       // this half's 64 queries' -lse2 and -D*scale (+inf lse past the segment end: P = 0)
-      const int32_t qh = i * 128 + 64 * h + (t & 63);
+      const int32_t qh = qi * 128 + 64 * h + (t & 63);
       float nl = -INFINITY, nd = 0.f;
       if (t < 64 && qh < w.len) {
         const size_t hi = static_cast<size_t>(w.head) * p.total + w.beg + qh;
@@ -471,7 +546,7 @@ __device__ __forceinline__ void bwd_elementwise(const BwdParams& p, uint8_t* sme
       if (__any_sync(0xffffffffu, !ok)) { ok = false; break; }
       s_ph ^= 1u;
       tc_fence_after();
-      if (PA_BWD_POLY_PAIRS > 0 && (i + 1) * 128 <= w.len)
+      if (PA_BWD_POLY_PAIRS > 0 && (qi + 1) * 128 <= w.len)
         bwd_ew_units<D, PA_BWD_POLY_PAIRS>(tA, tB, stage, ds_blk, h, t, key_ok, c2, sc2, ek);
       else
         bwd_ew_units<D, 0>(tA, tB, stage, ds_blk, h, t, key_ok, c2, sc2, ek);
@@ -492,7 +567,7 @@ __device__ __forceinline__ void bwd_elementwise(const BwdParams& p, uint8_t* sme
 // Warps 12-15: per tile the dQ partial of query row i*128 + t, one column half at a time
 // (each half's columns are released as soon as they are in registers, for the next
 // dP^T half), into the fp32 reductions; at the end of the item dV and dK of key row t.
-template <int D>
+template <int D, bool kSparse>
 __device__ __forceinline__ void bwd_reduce_store(const BwdParams& p, BwdBars* bars, const WaitCtl& wc, uint32_t tmem) {
   using C = BwdCfg<D>;
   const int t = threadIdx.x & 127;
@@ -509,13 +584,24 @@ __device__ __forceinline__ void bwd_reduce_store(const BwdParams& p, BwdBars* ba
     __syncwarp();
     if (lane == 0 && got != -2) mbar_arrive(&bars->sched_empty[(sk - 1) & 1]);
     if (got <= 0) break;
+    if (kSparse && w.nq == 0) {  // nobody names this key block
+      if (t < w.len - w.k0) {
+        const size_t row = (static_cast<size_t>(w.beg + w.k0 + t) * p.heads + w.head) * D;
+        for (int c = 0; c < D; c += 8)
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.dv) + row + c) =
+              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.dk) + row + c) = make_uint4(0u, 0u, 0u, 0u);
+      }
+      continue;
+    }
     bool ok = true;
+    BwdQueryWalk<kSparse> walk(p, w);
     for (int32_t i = 0; i < w.nq; ++i) {
+      const int32_t qi = walk.next(i);
       ok = mbar_wait(&bars->dq_full, dqf_ph, wc);
       if (__any_sync(0xffffffffu, !ok)) { ok = false; break; }
       dqf_ph ^= 1u;
       tc_fence_after();
-      const int32_t qrow = i * 128 + t;
+      const int32_t qrow = qi * 128 + t;
       const bool row_ok = qrow < w.len;
       const size_t tok = static_cast<size_t>(w.beg) + qrow;
       float* base = p.dq_acc + (static_cast<size_t>(w.head) * (D / 4) * p.total + tok) * 4;
@@ -571,7 +657,7 @@ __device__ __forceinline__ void bwd_reduce_store(const BwdParams& p, BwdBars* ba
 }
 
 // ------------------------------------------------------------------ kernels
-template <int D>
+template <int D, bool kSparse = false>
 __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_kernel(const __grid_constant__ BwdParams p) {
   using C = BwdCfg<D>;
   extern __shared__ uint8_t smem_raw[];
@@ -615,13 +701,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_kernel(const __grid_c
   const int32_t n_items = p.counts[0];
   const int32_t n_sorted = p.counts[1];
   if (warp < 8) {
-    bwd_elementwise<D>(p, smem, bars, wc, tmem, warp >> 2);
+    bwd_elementwise<D, kSparse>(p, smem, bars, wc, tmem, warp >> 2);
   } else if (warp >= 12) {
-    bwd_reduce_store<D>(p, bars, wc, tmem);
+    bwd_reduce_store<D, kSparse>(p, bars, wc, tmem);
   } else if (warp == 8) {
-    if ((threadIdx.x & 31) == 0) bwd_producer<D>(p, smem, bars, wc, n_items, n_sorted);
+    if ((threadIdx.x & 31) == 0) bwd_producer<D, kSparse>(p, smem, bars, wc, n_items, n_sorted);
   } else if (warp == 9) {
-    bwd_mma<D>(p, smem, bars, wc, tmem);  // the whole warp; one elected lane issues
+    bwd_mma<D, kSparse>(p, smem, bars, wc, tmem);  // the whole warp; one elected lane issues
   }
   __syncwarp();
   tc_fence_before();

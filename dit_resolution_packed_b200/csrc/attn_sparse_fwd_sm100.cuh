@@ -1,0 +1,433 @@
+// attn_sparse_fwd_sm100.cuh -- packed attention over listed key blocks, forward, for B200 (sm_100a).
+//
+// Math, softmax and tensor-memory layout are those of attn_fwd_sm100.cuh (whose tile code it uses); what differs is
+// which K and V tiles meet which query tile.  A work item is (segment, head, pair of 128-row query tiles); each of
+// the two tiles has a list of its own.  The plan kernel (sparse_plan_sm100.cuh) has merged them into steps: in step
+// j tile 0 meets one key block and tile 1 another, and blocks that both name come first and are loaded once for
+// both.  So the ping-pong of the dense kernel (one tile's softmax behind the other's products) goes on whatever the
+// lists hold, and a list's order does not matter to the result beyond its rounding.
+//
+// Ring of K/V tiles, in the order the MMA warp takes them (tile t is active in steps [0, cnt_t)):
+//     K0_0, K1_0,  then per step j:  V0_j, K0_{j+1}, V1_j, K1_{j+1}     (a shared tile appears once, as tile 0's).
+// Unshared steps move 4 tiles of 128 d 2 bytes per two score tiles, twice the dense kernel's; from L2, which holds
+// a head's K and V.  A tile without keys writes zeros and lse = -infinity and takes part in nothing else.
+//
+// Warps as in the dense kernel: 0-3 and 4-7 softmax and epilogue of tiles 0 and 1, 8 TMA producer, 9 MMA issuer.
+#pragma once
+#include "attn_fwd_sm100.cuh"
+#include "sparse_plan_sm100.cuh"
+
+namespace pa {
+
+struct SparseFwdParams {
+  const int32_t* counts;  // [0] items
+  int32_t* next_item;
+  const int32_t* order;   // nullptr: items as they lie
+  const int32_t* desc;    // [items][kDescInts]
+  const int2* steps;      // [items][width]
+  const uint8_t* maps;    // [B][3] tensor maps: q, k, v
+  void* out;
+  float* lse;
+  int32_t* status;
+  int32_t heads, width;
+  float scale_log2;
+  uint64_t wait_limit_ns;
+  int32_t err_timeout;
+};
+
+struct SparseBars {
+  uint64_t q_full, q_empty;
+  uint64_t kv_full[12], kv_empty[12];
+  uint64_t s_full[2], o_full[2], o_empty[2];
+  uint64_t p_full[2][2];
+  uint64_t sched_full[2], sched_empty[2];
+  uint64_t drain;
+  int32_t sched_item[2][kDescInts];
+  uint32_t tmem_base;
+  int abort_flag;
+};
+static_assert(sizeof(SparseBars) <= 512, "barrier block");
+
+struct SparseItem {
+  int32_t seg, beg, len, head, q0;
+  int32_t cnt0, cnt1;        // steps of tile 0 and of tile 1
+  int32_t common;            // of them shared
+  int32_t ragged0, ragged1;  // the tile's step with the segment's short last block, or -1
+  bool two;
+  __device__ __forceinline__ int32_t steps() const { return max(cnt0, cnt1); }
+  __device__ __forceinline__ int32_t cnt(int tile) const { return tile ? cnt1 : cnt0; }
+};
+
+__device__ __forceinline__ SparseItem sparse_item(const volatile int32_t* d) {
+  SparseItem w;
+  w.seg = d[0];
+  w.beg = d[1];
+  w.len = d[2];
+  w.head = d[3];
+  w.q0 = d[4];
+  w.cnt0 = d[5];
+  w.cnt1 = d[6];
+  w.common = d[7];
+  w.ragged0 = d[8];
+  w.ragged1 = d[9];
+  w.two = d[10] != 0;
+  return w;
+}
+
+// Next item from the producer's ring: 1 with `w`, 0 when done, -2 when the wait gave up.
+__device__ __forceinline__ int sparse_next(SparseBars* bars, uint32_t& sk, const WaitCtl& wc, SparseItem& w) {
+  const int ss = sk & 1;
+  const uint32_t sph = (sk >> 1) & 1u;
+  ++sk;
+  if (!mbar_wait(&bars->sched_full[ss], sph, wc)) return -2;
+  w = sparse_item(bars->sched_item[ss]);
+  return w.seg < 0 ? 0 : 1;
+}
+
+template <int D>
+__device__ __forceinline__ void sparse_producer(const SparseFwdParams& p, uint8_t* smem, SparseBars* bars,
+                                                const WaitCtl& wc) {
+  using C = FwdCfg<D>;
+  int slot = 0;
+  uint32_t phase = 0, q_round = 0, sk = 0;
+  uint32_t armed = 0, armed_phase = 0;
+  bool q_armed = false;
+  uint32_t q_armed_phase = 0;
+  bool ok = true;
+  const int32_t n_items = p.counts[0];
+  auto load_tile = [&](const void* map, int32_t xcol, int32_t block) -> bool {
+    if (!mbar_wait(&bars->kv_empty[slot], phase ^ 1u, wc)) return false;
+    mbar_arrive_expect_tx(&bars->kv_full[slot], C::kTileBytes);
+    armed |= 1u << slot;
+    armed_phase = (armed_phase & ~(1u << slot)) | (phase << slot);
+    uint8_t* dst = smem + C::kOffKV + slot * C::kTileBytes;
+#pragma unroll
+    for (int cb = 0; cb < C::kColBlocks; ++cb)
+      tma_load_2d(dst + cb * C::kBlockBytes, map, xcol + cb * 64, block * 128, &bars->kv_full[slot]);
+    if (++slot == C::kSlots) {
+      slot = 0;
+      phase ^= 1u;
+    }
+    return true;
+  };
+  for (;;) {
+    const int ss = sk & 1;
+    const uint32_t sph = (sk >> 1) & 1u;
+    ++sk;
+    if (!(ok = mbar_wait(&bars->sched_empty[ss], sph ^ 1u, wc))) break;
+    int32_t item = -1;
+    const int32_t* d = nullptr;
+    for (;;) {  // rows of the work list that hold no item are passed over
+      const int32_t at = atomicAdd(p.next_item, 1);
+      if (at >= n_items) {
+        item = -1;
+        break;
+      }
+      item = p.order != nullptr ? __ldg(p.order + at) : at;
+      d = p.desc + static_cast<int64_t>(item) * kDescInts;
+      if (__ldg(d) >= 0) break;
+    }
+    volatile int32_t* to = bars->sched_item[ss];
+    if (item < 0) {
+      to[0] = -1;
+      mbar_arrive(&bars->sched_full[ss]);
+      break;
+    }
+#pragma unroll
+    for (int i = 0; i < kDescInts; ++i) to[i] = __ldg(d + i);
+    const SparseItem w = sparse_item(to);
+    mbar_arrive(&bars->sched_full[ss]);
+    const int32_t n = w.steps();
+    if (n == 0) continue;
+
+    const uint8_t* maps = p.maps + static_cast<size_t>(w.seg) * 3 * 128;
+    const void *mq = maps, *mk = maps + 128, *mv = maps + 256;
+    fence_tmap_acquire(mq);
+    fence_tmap_acquire(mk);
+    fence_tmap_acquire(mv);
+    const int32_t xcol = w.head * D;
+    if (!(ok = mbar_wait(&bars->q_empty, (q_round & 1u) ^ 1u, wc))) break;
+    mbar_arrive_expect_tx(&bars->q_full, (w.two ? 2u : 1u) * C::kTileBytes);
+    q_armed = true;
+    q_armed_phase = q_round & 1u;
+    ++q_round;
+#pragma unroll
+    for (int cb = 0; cb < C::kColBlocks; ++cb) {
+      tma_load_2d(smem + C::kOffQ + cb * C::kBlockBytes, mq, xcol + cb * 64, w.q0, &bars->q_full);
+      if (w.two)
+        tma_load_2d(smem + C::kOffQ + C::kTileBytes + cb * C::kBlockBytes, mq, xcol + cb * 64, w.q0 + 128,
+                    &bars->q_full);
+    }
+    const int2* steps = p.steps + static_cast<int64_t>(item) * p.width;
+    int2 cur = __ldg(steps);
+    if (w.cnt0 > 0 && !(ok = load_tile(mk, xcol, cur.x))) break;
+    if (w.cnt1 > 0 && w.common == 0 && !(ok = load_tile(mk, xcol, cur.y))) break;
+    for (int32_t j = 0; j < n; ++j) {
+      const bool more = j + 1 < n;
+      const int2 nxt = more ? __ldg(steps + j + 1) : cur;
+      if (j < w.cnt0) {
+        if (!(ok = load_tile(mv, xcol, cur.x))) break;
+        if (j + 1 < w.cnt0 && !(ok = load_tile(mk, xcol, nxt.x))) break;
+      }
+      if (j < w.cnt1) {
+        if (j >= w.common && !(ok = load_tile(mv, xcol, cur.y))) break;
+        if (j + 1 < w.cnt1 && j + 1 >= w.common && !(ok = load_tile(mk, xcol, nxt.y))) break;
+      }
+      cur = nxt;
+    }
+    if (!ok) break;
+  }
+  if (!ok) {
+    // Let every copy this thread started land before the CTA can exit.
+    for (int s = 0; s < C::kSlots; ++s)
+      if (armed & (1u << s)) drain_wait(&bars->kv_full[s], (armed_phase >> s) & 1u, wc.limit_ns);
+    if (q_armed) drain_wait(&bars->q_full, q_armed_phase, wc.limit_ns);
+  }
+}
+
+template <int D>
+__device__ __forceinline__ void sparse_mma(uint8_t* smem, SparseBars* bars, const WaitCtl& wc, uint32_t tmem) {
+  using C = FwdCfg<D>;
+  const uint32_t q_addr0 = smem_u32(smem + C::kOffQ);
+  const uint32_t kv_addr0 = smem_u32(smem + C::kOffKV);
+  const uint32_t ones_addr = smem_u32(smem + C::kOffOnes);
+  int slot = 0;
+  uint32_t phase = 0, q_round = 0;
+  uint32_t p_ph = 0, oe_ph = 0;  // bit t: phase of tile t
+  uint32_t sk = 0;
+  bool ok = true;
+  const uint32_t leader = elect_one_sync();
+  // the ring's next tile, loaded; returns its slot
+  auto take = [&](bool& good) -> int {
+    const int s = slot;
+    good = mbar_wait(&bars->kv_full[slot], phase, wc);
+    if (++slot == C::kSlots) {
+      slot = 0;
+      phase ^= 1u;
+    }
+    return s;
+  };
+  for (;;) {
+    SparseItem w;
+    const int got = sparse_next(bars, sk, wc, w);
+    if (got != -2 && leader) mbar_arrive(&bars->sched_empty[(sk - 1) & 1]);
+    if (got == -2) ok = false;
+    if (got <= 0) break;
+    const int32_t n = w.steps();
+    if (n == 0) continue;
+    if (!(ok = mbar_wait(&bars->q_full, q_round & 1u, wc))) break;
+    ++q_round;
+    int ks = 0, vs = 0;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      if (w.cnt(t) == 0) continue;
+      if (t == 0 || w.common == 0) {
+        ks = take(ok);
+        if (!ok) break;
+      }
+      tc_fence_after();
+      issue_s<D>(leader, tmem + C::col_s(t), q_addr0 + t * C::kTileBytes, kv_addr0 + ks * C::kTileBytes);
+      mma_commit_if(leader, &bars->s_full[t]);
+      if (t == 1 || w.common == 0) mma_commit_if(leader, &bars->kv_empty[ks]);
+    }
+    if (!ok) break;
+    if (n == 1) mma_commit_if(leader, &bars->q_empty);
+    for (int32_t j = 0; j < n; ++j) {
+      const bool shared = j < w.common, shared_next = j + 1 < w.common;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if (j >= w.cnt(t)) continue;
+        if (t == 0 || !shared) {
+          vs = take(ok);
+          if (!ok) break;
+        }
+        if (j == 0) {
+          if (!(ok = mbar_wait(&bars->o_empty[t], ((oe_ph >> t) & 1u) ^ 1u, wc))) break;
+          oe_ph ^= 1u << t;
+        }
+        if (!(ok = mbar_wait(&bars->p_full[t][0], (p_ph >> t) & 1u, wc))) break;
+        tc_fence_after();
+        issue_pv_half<D>(leader, tmem + C::col_o(t), tmem + C::col_s(t), kv_addr0 + vs * C::kTileBytes, ones_addr, 0,
+                         j > 0);
+        if (!(ok = mbar_wait(&bars->p_full[t][1], (p_ph >> t) & 1u, wc))) break;
+        p_ph ^= 1u << t;
+        tc_fence_after();
+        issue_pv_half<D>(leader, tmem + C::col_o(t), tmem + C::col_s(t), kv_addr0 + vs * C::kTileBytes, ones_addr, 1,
+                         true);
+        if (t == 1 || !shared) mma_commit_if(leader, &bars->kv_empty[vs]);
+        if (j + 1 < w.cnt(t)) {
+          if (t == 0 || !shared_next) {
+            ks = take(ok);
+            if (!ok) break;
+            tc_fence_after();
+          }
+          issue_s<D>(leader, tmem + C::col_s(t), q_addr0 + t * C::kTileBytes, kv_addr0 + ks * C::kTileBytes);
+          mma_commit_if(leader, &bars->s_full[t]);
+          if (t == 1 || !shared_next) mma_commit_if(leader, &bars->kv_empty[ks]);
+        } else {
+          mma_commit_if(leader, &bars->o_full[t]);
+        }
+      }
+      if (!ok) break;
+      if (j + 2 == n) mma_commit_if(leader, &bars->q_empty);  // every S of the item is issued
+    }
+    if (!ok) break;
+  }
+  // Every MMA issued so far completes before tensor memory is released.
+  mma_commit_if(leader, &bars->drain);
+  drain_wait(&bars->drain, 0, wc.limit_ns);
+}
+
+template <int D>
+__device__ __forceinline__ void sparse_softmax(const SparseFwdParams& p, SparseBars* bars, const WaitCtl& wc,
+                                               uint32_t tmem, int tile) {
+  using C = FwdCfg<D>;
+  const int t = threadIdx.x & 127;  // row of the query tile
+  const int lane = threadIdx.x & 31;
+  const uint32_t lane_base = static_cast<uint32_t>(t & ~31) << 16;
+  const uint32_t tS = tmem + lane_base + C::col_s(tile);
+  const uint32_t tO = tmem + lane_base + C::col_o(tile);
+  const float c = p.scale_log2;
+  uint32_t s_ph = 0, of_ph = 0, sk = 0;
+  bool ok = true;
+  for (;;) {
+    SparseItem w;
+    int got = sparse_next(bars, sk, wc, w);
+    if (__any_sync(0xffffffffu, got == -2)) got = -2;
+    __syncwarp();
+    if (lane == 0 && got != -2) mbar_arrive(&bars->sched_empty[(sk - 1) & 1]);
+    if (got <= 0) break;
+    const int32_t row = w.q0 + tile * 128 + t;  // row of the segment
+    const bool row_ok = row < w.len;
+    const size_t at = (static_cast<size_t>(w.beg) + (row_ok ? row : w.q0)) * p.heads + w.head;
+    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at * D);
+    if (w.cnt(tile) == 0) {
+      if (row_ok) {
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) dst[i] = make_uint4(0u, 0u, 0u, 0u);
+        p.lse[at] = -INFINITY;
+      }
+      continue;
+    }
+    float m = 0.f, l = 0.f, lr = 0.f;
+    uint64_t* ph = bars->p_full[tile];
+    const int32_t n = w.cnt(tile), ragged = tile ? w.ragged1 : w.ragged0, tail = w.len & 127;
+    for (int32_t j = 0; j < n; ++j) {
+      ok = mbar_wait(&bars->s_full[tile], s_ph, wc);
+      if (__any_sync(0xffffffffu, !ok)) { ok = false; break; }
+      s_ph ^= 1u;
+      tc_fence_after();
+      uint64_t r[64];
+      tmem_ld128_pairs(tS, r);
+      if (j != ragged) {
+        if (c >= 0.f) softmax_tile<false, false, D>(r, 0, 128, j == 0, c, tS, tO, m, l, lr, ph, lane);
+        else softmax_tile<false, true, D>(r, 0, 128, j == 0, c, tS, tO, m, l, lr, ph, lane);
+      } else {
+        if (c >= 0.f) softmax_tile<true, false, D>(r, 0, tail, j == 0, c, tS, tO, m, l, lr, ph, lane);
+        else softmax_tile<true, true, D>(r, 0, tail, j == 0, c, tS, tO, m, l, lr, ph, lane);
+      }
+    }
+    if (!ok) break;
+
+    ok = mbar_wait(&bars->o_full[tile], of_ph, wc);
+    if (__any_sync(0xffffffffu, !ok)) { ok = false; break; }
+    of_ph ^= 1u;
+    tc_fence_after();
+    if (C::kSumColumn) {
+      uint32_t sc[16];
+      PA_TMEM_LD16(tO + D, sc);
+      tmem_wait_ld();
+      lr = __uint_as_float(sc[0]);
+    }
+    const float inv_l = 1.0f / lr;
+#pragma unroll
+    for (int cc = 0; cc < D / 32; ++cc) {
+      uint32_t o[32];
+      PA_TMEM_LD32(tO + cc * 32, o);
+      tmem_wait_ld();
+#pragma unroll
+      for (int q4 = 0; q4 < 4; ++q4) {
+        uint4 v;
+        v.x = pack_bf16x2(__uint_as_float(o[q4 * 8 + 0]) * inv_l, __uint_as_float(o[q4 * 8 + 1]) * inv_l);
+        v.y = pack_bf16x2(__uint_as_float(o[q4 * 8 + 2]) * inv_l, __uint_as_float(o[q4 * 8 + 3]) * inv_l);
+        v.z = pack_bf16x2(__uint_as_float(o[q4 * 8 + 4]) * inv_l, __uint_as_float(o[q4 * 8 + 5]) * inv_l);
+        v.w = pack_bf16x2(__uint_as_float(o[q4 * 8 + 6]) * inv_l, __uint_as_float(o[q4 * 8 + 7]) * inv_l);
+        if (row_ok) dst[cc * 4 + q4] = v;
+      }
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars->o_empty[tile]);
+    if (row_ok) p.lse[at] = (m + __log2f(l)) * 0.69314718055994531f;
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kFwdThreads, 1) attn_sparse_fwd_kernel(const __grid_constant__ SparseFwdParams p) {
+  using C = FwdCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  SparseBars* bars = reinterpret_cast<SparseBars*>(smem + C::kOffBar);
+  const int warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    mbar_init(&bars->q_full, 1);
+    mbar_init(&bars->q_empty, 1);
+    for (int s = 0; s < C::kSlots; ++s) {
+      mbar_init(&bars->kv_full[s], 1);
+      mbar_init(&bars->kv_empty[s], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&bars->s_full[t], 1);
+      mbar_init(&bars->p_full[t][0], 4);
+      mbar_init(&bars->p_full[t][1], 4);
+      mbar_init(&bars->o_full[t], 1);
+      mbar_init(&bars->o_empty[t], 4);
+      mbar_init(&bars->sched_full[t], 1);
+      mbar_init(&bars->sched_empty[t], 9);  // the MMA thread + one lane of each softmax warp
+    }
+    mbar_init(&bars->drain, 1);
+    bars->abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (C::kSumColumn) {
+    // the tile of ones read by P.V as V's extra columns (bf16 1.0 = 0x3F80)
+    uint4* ones = reinterpret_cast<uint4*>(smem + C::kOffOnes);
+    for (int i = threadIdx.x; i < C::kRows * 128 / 16; i += kFwdThreads)
+      ones[i] = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
+    fence_proxy_async_smem();
+  }
+  if (warp == 9) {
+    tmem_alloc(&bars->tmem_base, C::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+  const WaitCtl wc{&bars->abort_flag, p.status, p.wait_limit_ns, p.err_timeout};
+  // Everything above overlaps the plan kernel (programmatic dependent launch); the work list and the tensor maps
+  // are read only after it has completed.
+  pdl_wait_primary();
+  if (warp < 8) {
+    regs_increase<kSoftmaxRegs>();
+    sparse_softmax<D>(p, bars, wc, tmem, warp >> 2);
+    tc_fence_before();
+    named_bar_sync(1, kFwdThreads);
+  } else {
+    regs_decrease<kControlRegs>();
+    if (warp == 8) {
+      if ((threadIdx.x & 31) == 0) sparse_producer<D>(p, smem, bars, wc);
+    } else if (warp == 9) {
+      sparse_mma<D>(smem, bars, wc, tmem);  // the whole warp; one elected lane issues
+    }
+    __syncwarp();
+    tc_fence_before();
+    named_bar_sync(1, kFwdThreads);
+    if (warp == 9) {
+      tc_fence_after();
+      tmem_dealloc(tmem, C::kTmemCols);
+    }
+  }
+}
+
+}  // namespace pa

@@ -1,0 +1,454 @@
+// sparse_plan_sm100.cuh -- which key blocks a block of queries sees: the selection by a cheap score, and the work
+// lists of the block-sparse attention kernels.
+//
+// A pack's blocks of 128 tokens are numbered along the stream: block b of segment s is row cu[s] / 128 + s + b of
+// the tables (integer division).  cu[s] / 128 + s grows strictly with s and a segment's blocks never reach its
+// successor's first row, so a row names one block, the segment of a row is found by binary search, and no table
+// size has to be read back from the device.  Pairs of blocks (256) and groups of eight (1024) are numbered alike.
+//
+// Selection.  The score of (query block, key block) is the inner product of their mean vectors.  Means, products
+// and sums are fp64: a sum of 128 bf16 values is exact there, so the order of two scores does not depend on the
+// order of the additions, and a selection can be reproduced.  It reads q and k once (memory-bound); the scores
+// themselves are d products per pair of blocks, 1/16384 of the attention's.
+#pragma once
+#include <cuda.h>
+
+#include <cstdint>
+
+#include "sm100_ptx.cuh"
+
+namespace pa {
+
+constexpr int kSparseBuckets = 1024;  // longest-first order: items of 1023 steps and more share the first bucket
+constexpr int kDescInts = 12;
+constexpr int kSelectMaxBlocks = 2048;  // key blocks of a segment in pa_block_select (8 rows of scores in shared memory)
+
+// A segment of the pack and a unit (block, pair or group of 2^log2 tokens) of it; valid: the unit has tokens.
+struct UnitAt {
+  int32_t seg, beg, len, unit;
+  bool valid;
+};
+
+// The unit of a row of a table.  Reads cu_seqlens only inside [0, batch]; a segment that does not lie in
+// [0, total], or is longer than max_seqlen, has no units.
+__device__ __forceinline__ UnitAt unit_at(const int32_t* cu, int32_t batch, int32_t total, int32_t max_seqlen,
+                                          int64_t row, int log2) {
+  int32_t lo = 0, hi = batch;
+  while (hi - lo > 1) {
+    const int32_t mid = (lo + hi) >> 1;
+    if ((static_cast<int64_t>(__ldg(cu + mid)) >> log2) + mid <= row) lo = mid; else hi = mid;
+  }
+  UnitAt u;
+  u.seg = lo;
+  u.beg = __ldg(cu + lo);
+  const int32_t end = __ldg(cu + lo + 1);
+  const bool ok = u.beg >= 0 && end > u.beg && end <= total && end - u.beg <= max_seqlen;
+  u.len = ok ? end - u.beg : 0;
+  const int64_t first = (static_cast<int64_t>(u.beg) >> log2) + lo;
+  const int64_t unit = row - first;
+  u.valid = ok && unit >= 0 && unit < ((static_cast<int64_t>(u.len) + (1 << log2) - 1) >> log2);
+  u.unit = u.valid ? static_cast<int32_t>(unit) : 0;
+  return u;
+}
+
+// Records what is wrong with cu_seqlens (one block).
+__device__ __forceinline__ void check_pack(const int32_t* cu, int32_t batch, int32_t total, int32_t max_seqlen,
+                                           int32_t* status, int32_t err_cu, int32_t err_max) {
+  if (threadIdx.x == 0 && (cu[0] != 0 || cu[batch] != total)) atomicCAS(status, 0, err_cu);
+  for (int32_t i = threadIdx.x; i < batch; i += blockDim.x) {
+    const int32_t a = cu[i], b = cu[i + 1];
+    if (b < a) atomicCAS(status, 0, err_cu);
+    else if (static_cast<int64_t>(b) - a > max_seqlen) atomicCAS(status, 0, err_max);
+  }
+}
+
+// ---------------------------------------------------------------- selection
+struct SelectParams {
+  const uint16_t* x[2];  // q, k: bf16 [T, H, d]
+  const int32_t* cu;
+  int32_t batch, total, heads, head_dim, max_seqlen, width, min_blocks;
+  double density;
+  double* mean;  // [2][H][rows][d]
+  int64_t rows;
+  int32_t* idx;  // [H][rows][width]
+  int32_t* cnt;  // [H][rows]
+  int32_t* status;
+  int32_t err_cu, err_max;
+};
+
+constexpr int kPoolThreads = 256;
+
+// Means of one block of tokens over 256 channels of q (z = 0) or k (z = 1): 8 warps take 16 tokens each, a lane 8
+// channels, and the warps' sums meet in shared memory.
+__global__ void __launch_bounds__(kPoolThreads) select_pool_kernel(const __grid_constant__ SelectParams p) {
+  __shared__ double acc[8][256];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int64_t row = blockIdx.x;
+  const int which = blockIdx.z;
+  const int32_t channels = p.heads * p.head_dim;
+  const int32_t c0 = blockIdx.y * 256 + lane * 8;
+  if (blockIdx.x == 0 && blockIdx.y == 0 && which == 0)
+    check_pack(p.cu, p.batch, p.total, p.max_seqlen, p.status, p.err_cu, p.err_max);
+  const UnitAt u = unit_at(p.cu, p.batch, p.total, p.max_seqlen, row, 7);
+  if (!u.valid) {
+    // a row that is no block: an empty list (for the heads whose first channel is among these 256)
+    if (which == 0) {
+      const int h0 = (blockIdx.y * 256 + p.head_dim - 1) / p.head_dim;
+      const int h1 = min(p.heads, static_cast<int>((blockIdx.y * 256 + 256 + p.head_dim - 1) / p.head_dim));
+      for (int h = h0; h < h1; ++h) {
+        const int64_t at = static_cast<int64_t>(h) * p.rows + row;
+        if (threadIdx.x == 0) p.cnt[at] = 0;
+        for (int i = threadIdx.x; i < p.width; i += kPoolThreads) p.idx[at * p.width + i] = -1;
+      }
+    }
+    return;
+  }
+  const int32_t tokens = min(128, u.len - u.unit * 128);
+  double s[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s[i] = 0.0;
+  if (c0 < channels) {
+    const uint16_t* src = p.x[which] + (static_cast<size_t>(u.beg) + u.unit * 128) * channels + c0;
+#pragma unroll 8
+    for (int t = w; t < tokens; t += 8) {
+      float v[8];
+      bf16x8_to_f32(__ldg(reinterpret_cast<const uint4*>(src + static_cast<size_t>(t) * channels)), v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[i] += static_cast<double>(v[i]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) acc[w][i * 32 + lane] = s[i];
+  __syncthreads();
+  const int c = blockIdx.y * 256 + threadIdx.x;
+  if (c >= channels) return;
+  double t = 0.0;
+  const int at = (threadIdx.x & 7) * 32 + (threadIdx.x >> 3);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) t += acc[i][at];
+  const int h = c / p.head_dim;
+  p.mean[((static_cast<int64_t>(which) * p.heads + h) * p.rows + row) * p.head_dim + (c - h * p.head_dim)] = t / tokens;
+}
+
+// Monotone map of a score to an unsigned integer; a NaN counts as -infinity, -0 as 0.
+__device__ __forceinline__ uint64_t score_key(double s) {
+  if (!(s == s)) s = -INFINITY;
+  const uint64_t b = static_cast<uint64_t>(__double_as_longlong(s + 0.0));
+  return (b >> 63) ? ~b : (b | (1ull << 63));
+}
+
+// One block per (group of 8 query blocks, head); warp w selects for query block w of the group.
+template <int D>
+__global__ void __launch_bounds__(256) select_topk_kernel(const __grid_constant__ SelectParams p) {
+  extern __shared__ double sm[];
+  double* qs = sm;                          // [8][D]
+  double* ks = qs + 8 * D;                  // [32][D + 1]: a chunk of key blocks (odd stride: no bank conflicts)
+  uint64_t* keys = reinterpret_cast<uint64_t*>(ks + 32 * (D + 1));  // [8][nb]
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int h = blockIdx.y;
+  const UnitAt u = unit_at(p.cu, p.batch, p.total, p.max_seqlen, blockIdx.x, 10);
+  if (!u.valid) return;
+  const int nb = (u.len + 127) >> 7;
+  const int q0 = u.unit * 8, nq = min(8, nb - q0);
+  const int64_t row0 = (u.beg >> 7) + u.seg;  // of the segment's first block
+  const double* qm = p.mean + (static_cast<int64_t>(h) * p.rows + row0) * D;
+  const double* km = qm + static_cast<int64_t>(p.heads) * p.rows * D;
+  for (int i = threadIdx.x; i < nq * D; i += 256) qs[i] = qm[q0 * D + i];
+  uint64_t* mine = keys + static_cast<size_t>(w) * nb;
+  for (int k0 = 0; k0 < nb; k0 += 32) {
+    const int n = min(32, nb - k0);
+    __syncthreads();  // the last chunk's readers are done
+    for (int i = threadIdx.x; i < n * D; i += 256) ks[(i / D) * (D + 1) + i % D] = km[static_cast<int64_t>(k0) * D + i];
+    __syncthreads();
+    if (w < nq && lane < n) {
+      const double* a = qs + w * D;
+      const double* b = ks + lane * (D + 1);
+      double s0 = 0.0, s1 = 0.0, s2 = 0.0, s3 = 0.0;
+#pragma unroll 4
+      for (int c = 0; c < D; c += 4) {
+        s0 = fma(a[c], b[c], s0);
+        s1 = fma(a[c + 1], b[c + 1], s1);
+        s2 = fma(a[c + 2], b[c + 2], s2);
+        s3 = fma(a[c + 3], b[c + 3], s3);
+      }
+      mine[k0 + lane] = score_key((s0 + s1) + (s2 + s3));
+    }
+  }
+  __syncwarp();
+  if (w >= nq) return;
+  const int keep = min(nb, max(p.min_blocks, static_cast<int>(ceil(p.density * static_cast<double>(nb)))));
+  // the largest threshold that at least `keep` scores reach, bit by bit from the top; done early when exactly
+  // `keep` reach it
+  uint64_t bar = 0;
+  int reached = nb;
+  for (int bit = 63; bit >= 0 && reached != keep; --bit) {
+    const uint64_t cand = bar | (1ull << bit);
+    int c = 0;
+    for (int i = lane; i < nb; i += 32) c += mine[i] >= cand;
+    c = __reduce_add_sync(0xffffffffu, c);
+    if (c >= keep) {
+      bar = cand;
+      reached = c;
+    }
+  }
+  // of the scores that equal the threshold, the lowest blocks are taken until `keep` are
+  int above = 0;
+  for (int i = lane; i < nb; i += 32) above += mine[i] > bar;
+  above = __reduce_add_sync(0xffffffffu, above);
+  int ties = keep - above, taken = 0;
+  const int64_t at = static_cast<int64_t>(h) * p.rows + row0 + q0 + w;
+  int32_t* out = p.idx + at * p.width;
+  const uint32_t below = (1u << lane) - 1u;
+  for (int i0 = 0; i0 < nb; i0 += 32) {
+    const int i = i0 + lane;
+    const uint64_t key = i < nb ? mine[i] : 0;
+    const bool over = i < nb && key > bar, tie = i < nb && key == bar;
+    const uint32_t mt = __ballot_sync(0xffffffffu, tie);
+    const bool pick = over || (tie && __popc(mt & below) < ties);
+    const uint32_t mp = __ballot_sync(0xffffffffu, pick);
+    if (pick) out[taken + __popc(mp & below)] = i;
+    ties -= __popc(mt);
+    taken += __popc(mp);
+  }
+  for (int i = keep + lane; i < p.width; i += 32) out[i] = -1;
+  if (lane == 0) p.cnt[at] = keep;
+}
+
+// ---------------------------------------------------------------- work lists
+struct SparsePlanParams {
+  CUtensorMap tmpl[4];     // q, k, v[, dout] over the whole [T, H*d] matrix
+  const void* base[4];
+  const int32_t* cu;
+  const int32_t* idx;      // [H][rows][width]
+  const int32_t* cnt;      // [H][rows]
+  int32_t batch, total, heads, max_seqlen, width, n_maps;
+  int64_t rows;            // block rows of the tables
+  int64_t units;           // rows of the work list per head: pairs (forward) or key blocks (backward)
+  uint64_t row_bytes;
+  int32_t* counts;         // [0] items, [2] work counter
+  int32_t* hist;           // [kSparseBuckets], zeroed before
+  int2* sort;              // [heads * units] (bucket or -1, rank in it)
+  int32_t* order;          // [heads * units] items, longest first
+  int32_t* desc;           // [heads * units][kDescInts]
+  int2* steps;             // forward: [heads * units][width]
+  uint32_t* bits;          // backward: [heads][rows][words] query blocks that name a key block, zeroed before
+  int32_t words;
+  uint8_t* maps;           // [batch][n_maps] tensor maps
+  int32_t sorted;          // 0: items are taken as they lie (no hist, sort, order)
+  int32_t* status;
+  int32_t err_cu, err_max, err_blocks;
+};
+
+// The segment's tensor maps: the templates with base and row extent moved, so that a tile's rows past the segment
+// read zeros and nothing of a neighbouring image (whatever it holds) enters a product.
+__device__ __forceinline__ void write_maps(const SparsePlanParams& p, const UnitAt& u, int lane) {
+  if (lane < p.n_maps) {
+    uint8_t* dst = p.maps + (static_cast<size_t>(u.seg) * p.n_maps + lane) * 128;
+    const uint4* src = reinterpret_cast<const uint4*>(&p.tmpl[lane]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) reinterpret_cast<uint4*>(dst)[i] = src[i];
+    tmap_replace_address(dst, static_cast<const uint8_t*>(p.base[lane]) + static_cast<uint64_t>(u.beg) * p.row_bytes);
+    tmap_replace_dim1(dst, static_cast<uint32_t>(u.len));
+    fence_tmap_release();
+  }
+}
+
+// Length of a block's list, 0 (and the status recorded) if it is not an increasing list of the segment's blocks.
+__device__ __forceinline__ int32_t checked_list(const SparsePlanParams& p, int64_t at, int32_t nb, int lane) {
+  const int32_t n = __ldg(p.cnt + at);
+  bool bad = n < 0 || n > p.width;
+  const int32_t m = bad ? 0 : n;
+  const int32_t* list = p.idx + at * p.width;
+  for (int32_t i = lane; i < m; i += 32) {
+    const int32_t v = __ldg(list + i);
+    bad |= v < 0 || v >= nb || (i > 0 && __ldg(list + i - 1) >= v);
+  }
+  if (__any_sync(0xffffffffu, bad)) {
+    if (lane == 0) atomicCAS(p.status, 0, p.err_blocks);
+    return 0;
+  }
+  return m;
+}
+
+__device__ __forceinline__ bool in_list(const int32_t* list, int32_t n, int32_t v) {
+  int32_t lo = 0, hi = n;
+  while (lo < hi) {
+    const int32_t mid = (lo + hi) >> 1;
+    if (__ldg(list + mid) < v) lo = mid + 1; else hi = mid;
+  }
+  return lo < n && __ldg(list + lo) == v;
+}
+
+// Bucket and rank of an item in the longest-first order.
+__device__ __forceinline__ void file_item(const SparsePlanParams& p, int64_t item, int32_t steps) {
+  if (!p.sorted) return;
+  const int bucket = min(steps, kSparseBuckets - 1);
+  p.sort[item] = make_int2(bucket, atomicAdd(p.hist + bucket, 1));
+}
+
+// Forward: one warp per (head, pair of query blocks).  The two lists become one list of steps: first the blocks
+// that both name (their K and V tiles are loaded once for both query tiles), then the others side by side, so both
+// tiles stay busy in every step but the last few and tile t is busy exactly in steps [0, cnt_t).
+__global__ void __launch_bounds__(128) sparse_plan_fwd_kernel(const __grid_constant__ SparsePlanParams p) {
+  const int lane = threadIdx.x & 31;
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  pdl_launch_dependents();
+  if (blockIdx.x == 0) {
+    check_pack(p.cu, p.batch, p.total, p.max_seqlen, p.status, p.err_cu, p.err_max);
+    if (!p.sorted && threadIdx.x == 0) {
+      p.counts[0] = static_cast<int32_t>(p.units * p.heads);
+      p.counts[2] = 0;
+    }
+  }
+  if (item >= p.units * p.heads) return;
+  const int32_t h = static_cast<int32_t>(item / p.units);
+  const UnitAt u = unit_at(p.cu, p.batch, p.total, p.max_seqlen, item - h * p.units, 8);
+  int32_t* d = p.desc + item * kDescInts;
+  if (!u.valid) {
+    if (lane == 0) {
+      d[0] = -1;
+      if (p.sorted) p.sort[item] = make_int2(-1, 0);
+    }
+    return;
+  }
+  if (h == 0 && u.unit == 0) write_maps(p, u, lane);
+  const int32_t nb = (u.len + 127) >> 7;
+  const bool two = u.unit * 256 + 128 < u.len;
+  const int64_t at0 = static_cast<int64_t>(h) * p.rows + (u.beg >> 7) + u.seg + 2 * u.unit;
+  const int32_t* l0 = p.idx + at0 * p.width;
+  const int32_t* l1 = l0 + p.width;
+  const int32_t n0 = checked_list(p, at0, nb, lane), n1 = two ? checked_list(p, at0 + 1, nb, lane) : 0;
+  int32_t common = 0;
+  if (n1 > 0)
+    for (int32_t i0 = 0; i0 < n0; i0 += 32)
+      common += __popc(__ballot_sync(0xffffffffu, i0 + lane < n0 && in_list(l1, n1, __ldg(l0 + min(i0 + lane, n0 - 1)))));
+  int2* steps = p.steps + item * p.width;
+  const uint32_t below = (1u << lane) - 1u;
+  int32_t c = 0, r = common;
+  for (int32_t i0 = 0; i0 < n0; i0 += 32) {
+    const bool have = i0 + lane < n0;
+    const int32_t v = __ldg(l0 + min(i0 + lane, n0 - 1));
+    const bool both = have && n1 > 0 && in_list(l1, n1, v);
+    const uint32_t mb = __ballot_sync(0xffffffffu, both), mh = __ballot_sync(0xffffffffu, have);
+    if (both) steps[c + __popc(mb & below)] = make_int2(v, v);
+    else if (have) steps[r + __popc(mh & ~mb & below)].x = v;
+    c += __popc(mb);
+    r += __popc(mh & ~mb);
+  }
+  r = common;
+  for (int32_t i0 = 0; i0 < n1; i0 += 32) {
+    const bool have = i0 + lane < n1;
+    const int32_t v = __ldg(l1 + min(i0 + lane, n1 - 1));
+    const bool alone = have && !(n0 > 0 && in_list(l0, n0, v));
+    const uint32_t ma = __ballot_sync(0xffffffffu, alone);
+    if (alone) steps[r + __popc(ma & below)].y = v;
+    r += __popc(ma);
+  }
+  if (lane == 0) {
+    // the step in which a tile meets the segment's last block, if that is a short one (the key mask)
+    const bool ragged = (u.len & 127) != 0;
+    const bool last0 = ragged && n0 > 0 && __ldg(l0 + n0 - 1) == nb - 1;
+    const bool last1 = ragged && n1 > 0 && __ldg(l1 + n1 - 1) == nb - 1;
+    d[0] = u.seg;
+    d[1] = u.beg;
+    d[2] = u.len;
+    d[3] = h;
+    d[4] = u.unit * 256;
+    d[5] = n0;
+    d[6] = n1;
+    d[7] = common;
+    d[8] = !last0 ? -1 : last1 ? common - 1 : n0 - 1;
+    d[9] = !last1 ? -1 : last0 ? common - 1 : n1 - 1;
+    d[10] = two ? 1 : 0;
+    d[11] = 0;
+    file_item(p, item, max(n0, n1));
+  }
+}
+
+// Backward, first: one warp per (head, query block) marks itself at every key block of its list.
+__global__ void __launch_bounds__(128) sparse_mark_kernel(const __grid_constant__ SparsePlanParams p) {
+  const int lane = threadIdx.x & 31;
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  if (blockIdx.x == 0) check_pack(p.cu, p.batch, p.total, p.max_seqlen, p.status, p.err_cu, p.err_max);
+  if (item >= p.rows * p.heads) return;
+  const int32_t h = static_cast<int32_t>(item / p.rows);
+  const UnitAt u = unit_at(p.cu, p.batch, p.total, p.max_seqlen, item - h * p.rows, 7);
+  if (!u.valid) return;
+  if (h == 0 && u.unit == 0) write_maps(p, u, lane);
+  const int32_t nb = (u.len + 127) >> 7;
+  const int32_t n = checked_list(p, item, nb, lane);
+  const int32_t* list = p.idx + item * p.width;
+  const int64_t first = item - u.unit;  // row of the segment's first block, in this head
+  for (int32_t i = lane; i < n; i += 32)
+    atomicOr(p.bits + (first + __ldg(list + i)) * p.words + (u.unit >> 5), 1u << (u.unit & 31));
+}
+
+// Backward, second: one warp per (head, key block) counts the query blocks that name it.
+__global__ void __launch_bounds__(128) sparse_plan_bwd_kernel(const __grid_constant__ SparsePlanParams p) {
+  const int lane = threadIdx.x & 31;
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  if (item >= p.rows * p.heads) return;
+  const int32_t h = static_cast<int32_t>(item / p.rows);
+  const UnitAt u = unit_at(p.cu, p.batch, p.total, p.max_seqlen, item - h * p.rows, 7);
+  int32_t* d = p.desc + item * kDescInts;
+  if (!u.valid) {
+    if (lane == 0) p.sort[item] = make_int2(-1, 0);
+    return;
+  }
+  int32_t n = 0;
+  for (int32_t i = lane; i < p.words; i += 32) n += __popc(p.bits[item * p.words + i]);
+  n = __reduce_add_sync(0xffffffffu, n);
+  if (lane == 0) {
+    d[0] = u.seg;
+    d[1] = u.beg;
+    d[2] = u.len;
+    d[3] = h;
+    d[4] = u.unit * 128;
+    d[5] = n;
+    file_item(p, item, n);
+  }
+}
+
+// Places the items longest first: every block forms the buckets' starts from the histogram.
+__global__ void __launch_bounds__(256) sparse_order_kernel(const __grid_constant__ SparsePlanParams p) {
+  __shared__ int32_t start[kSparseBuckets];
+  __shared__ int32_t warp_sum_s[8];
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  int32_t v[4], local = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[i] = p.hist[kSparseBuckets - 1 - (threadIdx.x * 4 + i)];
+    local += v[i];
+  }
+  int32_t x = local;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int32_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) warp_sum_s[w] = x;
+  __syncthreads();
+  int32_t before = x - local, all = 0;
+  for (int i = 0; i < 8; ++i) {
+    if (i < w) before += warp_sum_s[i];
+    all += warp_sum_s[i];
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    start[kSparseBuckets - 1 - (threadIdx.x * 4 + i)] = before;
+    before += v[i];
+  }
+  __syncthreads();
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    p.counts[0] = all;
+    p.counts[2] = 0;
+  }
+  const int64_t n = p.units * p.heads;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * 256) {
+    const int2 s = p.sort[i];
+    if (s.x >= 0) p.order[start[s.x] + s.y] = static_cast<int32_t>(i);
+  }
+}
+
+}  // namespace pa

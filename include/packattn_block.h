@@ -6,6 +6,8 @@
  *                                    front of the next
  *   pa_rope_axes / pa_qkv_rope_axes_fwd
  *                                    rotary positions with several axes (time, height, width)
+ *   pa_block_select, pa_block_sparse_attn_fwd / _bwd
+ *                                    attention over the key blocks that a cheap score selects
  *
  * Unlike packattn.h's entry points these take their scratch memory from the caller, so that two captured
  * graphs, or two streams, that use different buffers never share one; the library itself holds only the
@@ -138,6 +140,65 @@ PA_API int64_t pa_rope_axes_workspace_bytes(int32_t total_tokens, int32_t head_d
 PA_API int pa_qkv_rope_axes_fwd(const void* x, const void* w_qkv, const float* pos, int32_t total_tokens,
                                 int32_t hidden, int32_t heads, int32_t head_dim, const pa_rope_axes_desc* rope,
                                 void* q, void* k, void* v, void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * Block-sparse packed attention (SparseAttn page, sections 3.1-3.4: a softmax restricted to a kept set of
+ * keys).  Every segment is cut into blocks of 128 tokens from its first token on (the last one shorter); a
+ * block of queries sees the key blocks of its own segment that its list names.
+ *
+ * pa_block_rows -- rows of the list tables of a pack: total_tokens / 128 + batch (-1 if an argument is
+ * negative).  Block b of segment s is row cu_seqlens[s] / 128 + s + b (integer division).
+ *
+ *   idx   device, int32, [heads, pa_block_rows, width]: key blocks of the row's segment, increasing.
+ *   cnt   device, int32, [heads, pa_block_rows]: entries of the row's list, 0 .. width.  Entries past cnt, and
+ *         rows that are no block, are not read.
+ */
+PA_API int64_t pa_block_rows(int32_t batch, int32_t total_tokens);
+
+/*
+ * pa_block_select -- write idx and cnt: for each head and query block of a segment of nb blocks, the
+ *     min(nb, max(min_blocks, ceil(density * nb)))
+ * key blocks whose mean key has the largest inner product with the block's mean query, in increasing order
+ * (means and products in fp64; equal scores: the lower block first; a NaN score ranks last, as -infinity).
+ * Unused entries are -1, rows that are no block have cnt 0.
+ *   q, k          as for pa_varlen_attn_fwd.     max_seqlen  an upper bound of every segment, <= 262144.
+ *   density       0 .. 1 (fp64).                 min_blocks  >= 1.
+ *   width         at least the formula's value at nb = ceil(max_seqlen / 128), else PA_ERR_BLOCKS at once.
+ *   workspace     pa_block_select_workspace_bytes(...) bytes, 16-byte aligned.
+ */
+PA_API int64_t pa_block_select_workspace_bytes(int32_t batch, int32_t total_tokens, int32_t heads, int32_t head_dim);
+PA_API int pa_block_select(const void* q, const void* k, const int32_t* cu_seqlens, int32_t batch,
+                           int32_t total_tokens, int32_t heads, int32_t head_dim, int32_t max_seqlen, double density,
+                           int32_t min_blocks, int32_t width, int32_t* idx, int32_t* cnt, void* workspace,
+                           int64_t workspace_bytes, void* stream);
+
+/*
+ * pa_block_sparse_attn_fwd -- pa_varlen_attn_fwd restricted to the listed blocks (from pa_block_select or the
+ * caller's own pattern).  A row with an empty list gets out = 0 and lse = -infinity.  A list that is not
+ * increasing, names a block outside its segment, or has cnt outside 0 .. width is recorded as PA_ERR_BLOCKS in
+ * the status word, and out and lse are then undefined.
+ *   workspace     pa_block_sparse_workspace_bytes(..., backward = 0) bytes, 16-byte aligned.
+ * Bitwise deterministic.
+ */
+PA_API int64_t pa_block_sparse_workspace_bytes(int32_t batch, int32_t total_tokens, int32_t heads, int32_t head_dim,
+                                               int32_t max_seqlen, int32_t width, int32_t backward);
+PA_API int pa_block_sparse_attn_fwd(const void* q, const void* k, const void* v, const int32_t* cu_seqlens,
+                                    int32_t batch, int32_t total_tokens, int32_t heads, int32_t head_dim,
+                                    int32_t max_seqlen, const int32_t* idx, const int32_t* cnt, int32_t width,
+                                    float scale, void* out, float* lse, void* workspace, int64_t workspace_bytes,
+                                    void* stream);
+
+/*
+ * pa_block_sparse_attn_bwd -- its gradients (the lists are constants), arguments as for pa_varlen_attn_bwd and
+ * above; workspace with backward = 1.  A key block that no list names gets dk = dv = 0, a query with an empty
+ * list dq = 0.  dq sums fp32 partials of different key blocks in whatever order they arrive (its last bits may
+ * differ from run to run); dk and dv sum over query blocks in increasing order.
+ */
+PA_API int pa_block_sparse_attn_bwd(const void* q, const void* k, const void* v, const void* out, const float* lse,
+                                    const void* dout, const int32_t* cu_seqlens, int32_t batch, int32_t total_tokens,
+                                    int32_t heads, int32_t head_dim, int32_t max_seqlen, const int32_t* idx,
+                                    const int32_t* cnt, int32_t width, float scale, void* dq, void* dk, void* dv,
+                                    void* workspace, int64_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

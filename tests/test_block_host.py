@@ -180,3 +180,89 @@ def test_rope_refusals(lib):
         pa.rope_axes_fwd(q, q, pos.double(), [32, 32])
     with pytest.raises(TypeError):
         pa.rope_axes_fwd(q, q.float(), pos, [32, 32])
+
+
+# ---------------------------------------------------------------- attention over selected blocks
+
+BIG = 1 << 40
+
+
+def _select(lib, q=16, k=16, cu=16, batch=1, total=300, heads=2, d=64, longest=300, density=0.5, floor=1, width=2, idx=16,
+            cnt=16, ws=16, ws_bytes=BIG):
+    return lib.pa_block_select(q, k, cu, batch, total, heads, d, longest, density, floor, width, idx, cnt, ws, ws_bytes,
+                               None)
+
+
+def _sfwd(lib, q=16, k=16, v=16, cu=16, batch=1, total=300, heads=2, d=64, longest=300, idx=16, cnt=16, width=2,
+          scale=0.125, out=16, lse=16, ws=16, ws_bytes=BIG):
+    return lib.pa_block_sparse_attn_fwd(q, k, v, cu, batch, total, heads, d, longest, idx, cnt, width, scale, out, lse, ws,
+                                        ws_bytes, None)
+
+
+def _sbwd(lib, q=16, k=16, v=16, out=16, lse=16, dout=16, cu=16, batch=1, total=300, heads=2, d=64, longest=300, idx=16,
+          cnt=16, width=2, scale=0.125, dq=16, dk=16, dv=16, ws=16, ws_bytes=BIG):
+    return lib.pa_block_sparse_attn_bwd(q, k, v, out, lse, dout, cu, batch, total, heads, d, longest, idx, cnt, width,
+                                        scale, dq, dk, dv, ws, ws_bytes, None)
+
+
+def test_sparse_refusals(lib):
+    for call in (_select, _sfwd, _sbwd):
+        assert call(lib, d=96) == pa.PA_ERR_HEAD_DIM
+        assert call(lib, heads=0) == pa.PA_ERR_SHAPE
+        assert call(lib, heads=1 << 20) == pa.PA_ERR_SHAPE
+        assert call(lib, batch=-1) == pa.PA_ERR_SHAPE
+        assert call(lib, batch=0) == pa.PA_ERR_SHAPE
+        assert call(lib, total=-1) == pa.PA_ERR_SHAPE
+        assert call(lib, width=0) == pa.PA_ERR_SHAPE
+        assert call(lib, batch=0, total=0) == pa.PA_OK
+        assert call(lib, longest=0) == pa.PA_ERR_MAX_SEQLEN
+        for name in ("q", "k", "cu", "idx", "cnt"):
+            assert call(lib, **{name: None}) == pa.PA_ERR_NULL, name
+            assert call(lib, **{name: 18}) == pa.PA_ERR_ALIGN, name
+        assert call(lib, ws=None) == pa.PA_ERR_WORKSPACE
+        assert call(lib, ws=24) == pa.PA_ERR_WORKSPACE
+        assert call(lib, ws_bytes=1000) == pa.PA_ERR_WORKSPACE
+    assert _select(lib, density=-0.1) == pa.PA_ERR_SCALE and _select(lib, density=1.5) == pa.PA_ERR_SCALE
+    assert _select(lib, density=math.nan) == pa.PA_ERR_SCALE
+    assert _select(lib, floor=0) == pa.PA_ERR_SHAPE
+    assert _select(lib, width=1) == pa.PA_ERR_BLOCKS  # ceil(0.5 * 3) = 2 blocks
+    assert _select(lib, total=1 << 20, longest=262145) == pa.PA_ERR_MAX_SEQLEN
+    for call in (_sfwd, _sbwd):
+        assert call(lib, total=0) == pa.PA_OK
+        assert call(lib, scale=math.inf) == pa.PA_ERR_SCALE
+        for name in ("v", "out", "lse"):
+            assert call(lib, **{name: None}) == pa.PA_ERR_NULL, name
+        assert call(lib, v=8) == pa.PA_ERR_ALIGN and call(lib, lse=2) == pa.PA_ERR_ALIGN
+    for name in ("dout", "dq", "dk", "dv"):
+        assert _sbwd(lib, **{name: None}) == pa.PA_ERR_NULL
+        assert _sbwd(lib, **{name: 8}) == pa.PA_ERR_ALIGN
+
+
+def test_sparse_sizes(lib):
+    assert pa.pa_block_rows(3, 1000) == 10 and pa.pa_block_rows(-1, 5) == -1 and pa.pa_block_rows(1, -5) == -1
+    assert pa.pa_block_select_workspace_bytes(3, 1000, 2, 64) == 2 * 8 * 10 * 2 * 64
+    assert pa.pa_block_select_workspace_bytes(3, 1000, 2, 65) == -1
+    assert pa.pa_block_sparse_workspace_bytes(1, 300, 2, 65, 300, 2, 0) == -1
+    assert pa.pa_block_sparse_workspace_bytes(1, 300, 2, 64, -1, 2, 0) == -1
+    fwd, bwd = (pa.pa_block_sparse_workspace_bytes(1, 65536, 8, 64, 65536, 32, b) for b in (0, 1))
+    assert fwd > 8 * 256 * 32 * 8 and bwd > 65536 * 8 * 64 * 4
+    # an 8M-token pack: sizes past 32 bits
+    assert pa.pa_block_sparse_workspace_bytes(1, 1 << 23, 8, 128, 1 << 23, 64, 1) > 1 << 33
+
+
+def test_sparse_python_checks():
+    q = torch.zeros(300, 2, 64, dtype=torch.bfloat16)
+    cu = torch.tensor([0, 300], dtype=torch.int32)
+    idx, cnt = torch.zeros(2, 3, 2, dtype=torch.int32), torch.zeros(2, 3, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        pa.block_sparse_attn_fwd(q, q, q, cu, 300, idx[:, :2], cnt)
+    with pytest.raises(TypeError):
+        pa.block_sparse_attn_fwd(q, q, q, cu, 300, idx.long(), cnt)
+    with pytest.raises(ValueError):
+        pa.block_sparse_attn_fwd(q, q[:200], q, cu, 300, idx, cnt)
+    with pytest.raises(ValueError):
+        pa.block_sparse_attn_bwd(q, q, q, q, torch.zeros(2, 300), q, cu, 300, idx, cnt)
+    with pytest.raises(TypeError):
+        pa.block_select(q.float(), q, cu, 300, 0.5)
+    with pytest.raises(pa.PackAttnError):
+        pa.block_select(q, q, cu, 300, 2.0)

@@ -5,7 +5,6 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
-#include <type_traits>
 
 #include "block_norm_sm100.cuh"
 #include "host.h"
@@ -15,26 +14,43 @@ namespace {
 
 using pa::host::aligned;
 
-constexpr int kSms = 148;  // the chunking rules below must give one answer for the workspace and the launch
+// The splitting rules below give one answer for the workspace and the launch, so they use the number of SMs and of
+// warps that the kernels run with on a B200, not what a device reports.
+constexpr int kSms = 148;
+constexpr int kSmemPerSm = 208 * 1024;  // for rows in flight
 
-struct Split {
-  int32_t warps, groups, rows, chunks;
-  int threads() const { return warps * groups * 32; }
+// The backward's blocks: teams of threads that own the channels 8 (or 16, 32) a thread, runs of rows, and tiles of
+// them with row_warps warps a row; as many rows in flight as shared memory holds.  `rows`, `chunks` and `teams` (all
+// that the workspace depends on) follow from the sizes alone.
+struct BwdSplit {
+  int32_t vecs, team_warps, teams, per_sm, rows, chunks;
+  int32_t row_bytes, ring_offset, stages, tile, row_warps;
+  int threads() const { return 32 * teams * team_warps; }
+  size_t smem() const { return ring_offset + static_cast<size_t>(stages) * row_bytes; }
 };
-
-// A group of warps per row, as many groups as fit 8 warps, and chunks of rows.
-Split split_rows(int32_t total, int32_t hidden, int max_rows) {
-  Split s;
-  s.warps = (hidden + 255) / 256;
-  s.groups = std::max(1, 8 / s.warps);
-  const int64_t at_once = std::max<int64_t>(1, static_cast<int64_t>(kSms) * 16 / s.warps);
-  const int64_t want = (static_cast<int64_t>(total) + 2 * at_once - 1) / (2 * at_once);
-  s.rows = static_cast<int32_t>(std::min<int64_t>(std::max<int64_t>(want, 1), max_rows));
-  s.chunks = static_cast<int32_t>((static_cast<int64_t>(total) + s.rows - 1) / s.rows);
+BwdSplit split_bwd(int32_t total, int32_t hidden) {
+  BwdSplit s;
+  std::memset(&s, 0, sizeof(s));
+  s.vecs = hidden <= 2048 ? 1 : hidden <= 4096 ? 2 : 4;
+  s.team_warps = (hidden + 256 * s.vecs - 1) / (256 * s.vecs);
+  s.teams = 8 / s.team_warps;
+  s.per_sm = s.vecs == 1 ? 16 / (s.teams * s.team_warps) : 1;  // by the kernels' registers
+  s.rows = std::max(1, (total + kSms * s.per_sm - 1) / (kSms * s.per_sm));
+  s.chunks = (total + s.rows - 1) / s.rows;
   return s;
 }
-constexpr int kFwdRows = 32;
-constexpr int kBwdRows = 64;
+void split_bwd_rows(BwdSplit* s, int32_t hidden, int32_t row_bytes) {
+  s->row_bytes = row_bytes;
+  s->ring_offset = 8 * hidden;
+  const int warps = s->teams * s->team_warps;
+  s->stages = std::min(pa::kNormMaxBwdStages,
+                       std::max(1, (kSmemPerSm / s->per_sm - s->ring_offset) / std::max(1, row_bytes)));
+  // as few warps a row as keep three quarters of the block's warps at work on a tile's rows
+  s->row_warps = 1;
+  while (s->row_warps < warps && 4 * s->row_warps * std::min(warps / s->row_warps, s->stages) < 3 * warps)
+    s->row_warps *= 2;
+  s->tile = std::max(1, std::min({warps / s->row_warps, s->stages, pa::kNormMaxTile}));
+}
 
 int check_desc(const pa_block_norm_desc* d) {
   if (!d) return PA_ERR_NULL;
@@ -59,16 +75,13 @@ int check_desc(const pa_block_norm_desc* d) {
   return PA_OK;
 }
 
-pa::NormParams params_of(const pa_block_norm_desc* d, const Split& s) {
+pa::NormParams params_of(const pa_block_norm_desc* d, const pa::host::Call& call) {
   pa::NormParams p;
   std::memset(&p, 0, sizeof(p));
   p.cu = d->gate || d->scale || d->shift ? d->cu_seqlens : nullptr;
   p.total = d->total_tokens;
   p.batch = p.cu ? d->batch : 1;
   p.hidden = d->hidden;
-  p.rows_per_chunk = s.rows;
-  p.chunks = s.chunks;
-  p.warps = s.warps;
   p.post = d->post;
   p.pre = d->pre;
   p.param_f32 = d->param_fp32;
@@ -83,26 +96,67 @@ pa::NormParams params_of(const pa_block_norm_desc* d, const Split& s) {
   p.w_post = d->w_post;
   p.w_pre = d->w_pre;
   p.err_cu = PA_ERR_CU_SEQLENS;
+  p.err_timeout = PA_ERR_TIMEOUT;
+  p.status = call.status;
+  p.wait_limit_ns = call.wait_limit_ns;
   return p;
 }
 
-int64_t part_floats(int32_t batch, int32_t hidden, const Split& s) {
-  return (static_cast<int64_t>(s.chunks) + std::max(batch, 1)) * 3 * hidden;
+int64_t part_floats(int32_t batch, int32_t hidden, const BwdSplit& s) {
+  return (static_cast<int64_t>(s.chunks) + std::max(batch, 1)) * s.teams * 3 * hidden;
 }
 int64_t sum_floats(int32_t batch, int32_t hidden) { return 2 * static_cast<int64_t>(std::max(batch, 1)) * hidden; }
 
-template <class F>
-void by_type(int f32, int threads, F&& launch) {
-  // blocks of more than 256 threads hold one row of 2056 channels or more
-  if (f32) {
-    if (threads <= 256) launch(std::true_type{}, std::integral_constant<int, 256>{});
-    else if (threads <= 512) launch(std::true_type{}, std::integral_constant<int, 512>{});
-    else launch(std::true_type{}, std::integral_constant<int, 1024>{});
-  } else {
-    if (threads <= 256) launch(std::false_type{}, std::integral_constant<int, 256>{});
-    else if (threads <= 512) launch(std::false_type{}, std::integral_constant<int, 512>{});
-    else launch(std::false_type{}, std::integral_constant<int, 1024>{});
+// The forward's blocks: one per SM, groups of `warps` warps, each with a ring of rows behind the factors.
+struct FwdSplit {
+  int32_t warps, groups, rows, blocks, stages, row_bytes, ring_offset;
+  int threads() const { return warps * groups * 32; }
+  size_t smem() const { return ring_offset + static_cast<size_t>(groups) * stages * row_bytes; }
+};
+FwdSplit split_fwd(int32_t total, int32_t hidden, int32_t row_bytes) {
+  FwdSplit s;
+  s.warps = hidden <= 2048 ? 1 : hidden <= 4096 ? 2 : 4;
+  s.row_bytes = row_bytes;
+  s.ring_offset = 12 * hidden;
+  const int room = (kSmemPerSm - s.ring_offset) / row_bytes;  // rows
+  const int most = pa::kNormFwdThreads / 32 / s.warps;
+  s.rows = (total + kSms - 1) / kSms;
+  // rows for two groups of three to be worked on and for one on its way (with half as many groups the same time,
+  // with a group for every row no better); more where there is room, and no more groups than rows
+  s.groups = std::max(1, std::min({most, room * 2 / 3, s.rows}));
+  s.stages = std::max(1, std::min(pa::kNormMaxStages, room / s.groups));
+  s.blocks = (total + s.rows - 1) / s.rows;
+  return s;
+}
+
+// The kernels of a type, and of a split's warps (forward) or vectors (backward).
+template <bool kF32>
+struct Kernels {
+  static constexpr auto fwd1 = pa::block_norm_fwd_kernel<kF32, 1>;
+  static constexpr auto fwd2 = pa::block_norm_fwd_kernel<kF32, 2>;
+  static constexpr auto fwd4 = pa::block_norm_fwd_kernel<kF32, 4>;
+  static constexpr auto bwd1 = pa::block_norm_bwd_kernel<kF32, 1>;
+  static constexpr auto bwd2 = pa::block_norm_bwd_kernel<kF32, 2>;
+  static constexpr auto bwd4 = pa::block_norm_bwd_kernel<kF32, 4>;
+  static void (*fwd(int warps))(pa::NormFwdParams) { return warps == 1 ? fwd1 : warps == 2 ? fwd2 : fwd4; }
+  static void (*bwd(int vecs))(pa::NormBwdParams) { return vecs == 1 ? bwd1 : vecs == 2 ? bwd2 : bwd4; }
+  static bool allow_smem() {
+    for (int w : {1, 2, 4})
+      if (cudaFuncSetAttribute(fwd(w), cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemPerSm) != cudaSuccess)
+        return false;
+    for (int v : {1, 2, 4})
+      if (cudaFuncSetAttribute(bwd(v), cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemPerSm) != cudaSuccess)
+        return false;
+    return true;
   }
+};
+// Shared-memory limits, once per device (the caller holds the library's lock).
+int ensure_kernels(int dev) {
+  static bool ready[64] = {};
+  if (ready[dev]) return PA_OK;
+  if (!Kernels<false>::allow_smem() || !Kernels<true>::allow_smem()) return PA_ERR_CUDA;
+  ready[dev] = true;
+  return PA_OK;
 }
 
 }  // namespace
@@ -125,23 +179,28 @@ int pa_block_norm_fwd(const pa_block_norm_desc* d, const void* x, const void* y,
     return rc;
   pa::host::Call call(dev, stream);
   if (call.rc != PA_OK) return call.rc;
-  const Split s = split_rows(d->total_tokens, d->hidden, kFwdRows);
-  pa::NormParams p = params_of(d, s);
-  p.x = x;
-  p.y = y;
-  p.r = r;
-  p.z = z;
-  p.status = call.status;
-  const unsigned grid = static_cast<unsigned>((s.chunks + s.groups - 1) / s.groups);
-  by_type(d->residual_fp32, s.threads(), [&](auto f32, auto threads) {
-    pa::block_norm_fwd_kernel<f32.value, threads.value><<<grid, s.threads(), 0, call.stream>>>(p);
-  });
+  if ((rc = ensure_kernels(dev)) != PA_OK) return rc;
+  const FwdSplit s = split_fwd(d->total_tokens, d->hidden, d->hidden * ((d->residual_fp32 ? 4 : 2) + (y ? 2 : 0)));
+  pa::NormFwdParams f;
+  f.n = params_of(d, call);
+  f.n.rows_per_chunk = s.rows;
+  f.n.chunks = s.blocks;
+  f.n.stages = s.stages;
+  f.n.row_bytes = s.row_bytes;
+  f.n.x = x;
+  f.n.y = y;
+  f.n.r = r;
+  f.n.z = z;
+  f.groups = s.groups;
+  f.ring_offset = s.ring_offset;
+  const auto kernel = d->residual_fp32 ? Kernels<true>::fwd(s.warps) : Kernels<false>::fwd(s.warps);
+  kernel<<<s.blocks, s.threads(), s.smem(), call.stream>>>(f);
   return pa::host::launch_status();
 }
 
 int64_t pa_block_norm_workspace_bytes(int32_t batch, int32_t total_tokens, int32_t hidden) {
   if (batch < 0 || total_tokens < 0 || hidden < 8 || hidden > pa::kNormMaxHidden || hidden % 8 != 0) return -1;
-  const Split s = split_rows(total_tokens, hidden, kBwdRows);
+  const BwdSplit s = split_bwd(total_tokens, hidden);
   return 4 * (part_floats(batch, hidden, s) + sum_floats(batch, hidden));
 }
 
@@ -166,7 +225,9 @@ int pa_block_norm_bwd(const pa_block_norm_desc* d, const void* r, const void* y,
                           static_cast<const void*>(dshift), static_cast<const void*>(dw_post),
                           static_cast<const void*>(dw_pre)})
     if (!aligned(ptr, 16)) return PA_ERR_ALIGN;
-  const Split s = split_rows(d->total_tokens, d->hidden, kBwdRows);
+  BwdSplit s = split_bwd(d->total_tokens, d->hidden);
+  const int32_t wide = d->residual_fp32 ? 4 : 2;
+  split_bwd_rows(&s, d->hidden, d->hidden * ((dz ? wide + 2 : 0) + (dr ? wide : 0) + (y ? 2 : 0)));
   if (sums) {
     if (!workspace || !aligned(workspace, 16) ||
         workspace_bytes < pa_block_norm_workspace_bytes(d->batch, d->total_tokens, d->hidden))
@@ -182,7 +243,19 @@ int pa_block_norm_bwd(const pa_block_norm_desc* d, const void* r, const void* y,
     return rc;
   pa::host::Call call(dev, stream);
   if (call.rc != PA_OK) return call.rc;
-  pa::NormParams p = params_of(d, s);
+  if ((rc = ensure_kernels(dev)) != PA_OK) return rc;
+  pa::NormBwdParams b;
+  b.n = params_of(d, call);
+  b.tile = s.tile;
+  b.row_warps = s.row_warps;
+  b.teams = s.teams;
+  b.team_warps = s.team_warps;
+  b.ring_offset = s.ring_offset;
+  pa::NormParams& p = b.n;
+  p.rows_per_chunk = s.rows;
+  p.chunks = s.chunks;
+  p.stages = s.stages;
+  p.row_bytes = s.row_bytes;
   p.x = r;
   p.y = y;
   p.dr = dr;
@@ -190,12 +263,9 @@ int pa_block_norm_bwd(const pa_block_norm_desc* d, const void* r, const void* y,
   p.r = dx;
   p.z = dy;
   p.part = sums ? static_cast<float*>(workspace) : nullptr;
-  p.status = call.status;
   if (rows) {
-    const unsigned grid = static_cast<unsigned>((s.chunks + s.groups - 1) / s.groups);
-    by_type(d->residual_fp32, s.threads(), [&](auto f32, auto threads) {
-      pa::block_norm_bwd_kernel<f32.value, threads.value><<<grid, s.threads(), 0, call.stream>>>(p);
-    });
+    const auto kernel = d->residual_fp32 ? Kernels<true>::bwd(s.vecs) : Kernels<false>::bwd(s.vecs);
+    kernel<<<s.chunks, s.threads(), s.smem(), call.stream>>>(b);
     if ((rc = pa::host::launch_status()) != PA_OK) return rc;
   }
   if (!sums) return PA_OK;
@@ -213,6 +283,7 @@ int pa_block_norm_bwd(const pa_block_norm_desc* d, const void* r, const void* y,
   sp.hidden = p.hidden;
   sp.rows_per_chunk = p.rows_per_chunk;
   sp.chunks = p.chunks;
+  sp.teams = s.teams;
   sp.param_f32 = p.param_f32;
   sp.part = p.part;
   sp.sums = weights ? p.part + part_floats(d->batch, d->hidden, s) : nullptr;
@@ -221,7 +292,14 @@ int pa_block_norm_bwd(const pa_block_norm_desc* d, const void* r, const void* y,
   sp.dgate = dgate;
   sp.dscale = dscale;
   sp.dshift = dshift;
-  pa::block_norm_sum_kernel<<<dim3(p.batch, (p.hidden + 127) / 128), 256, 0, call.stream>>>(sp);
+  sp.use = (dgate || dw_post ? 1 : 0) | (dscale || dw_pre ? 2 : 0) | (dshift ? 4 : 0);
+  // 64 segments fill the GPU; with fewer, a segment's slots are read in parallel
+  if (p.batch > 64)
+    pa::block_norm_sum_kernel<<<dim3(p.batch, (p.hidden + 4 * pa::kNormSumThreads - 1) / (4 * pa::kNormSumThreads)),
+                                pa::kNormSumThreads, 0, call.stream>>>(sp);
+  else
+    pa::block_norm_sum_long_kernel<<<dim3(p.batch, (p.hidden + 127) / 128), pa::kNormSumLongThreads, 0, call.stream>>>(
+        sp);
   if ((rc = pa::host::launch_status()) != PA_OK || !weights) return rc;
   pa::NormWeightParams wp;
   std::memset(&wp, 0, sizeof(wp));

@@ -92,9 +92,11 @@ def test_norm_null_desc_and_workspace(lib):
     assert lib.pa_block_norm_bwd(None, *([16] * 11), 16, 0, None) == pa.PA_ERR_NULL
     assert pa.pa_block_norm_workspace_bytes(-1, 4, 64) == -1
     assert pa.pa_block_norm_workspace_bytes(1, 4, 65) == -1
-    # per chunk of rows and per image, three rows of channels, and two more per image
-    assert pa.pa_block_norm_workspace_bytes(2, 0, 64) == 4 * (2 * 3 + 2 * 2) * 64
-    assert pa.pa_block_norm_workspace_bytes(1, 2 ** 31 - 1, 8192) > 2 ** 40
+    # per image three rows of channels for each of 8 teams, and two more
+    assert pa.pa_block_norm_workspace_bytes(2, 0, 64) == 4 * (2 * 8 * 3 + 2 * 2) * 64
+    # runs of rows, not rows: bounded however long the pack is
+    assert 0 < pa.pa_block_norm_workspace_bytes(1, 2 ** 31 - 1, 8192) < 2 ** 28
+    assert pa.pa_block_norm_workspace_bytes(2 ** 20, 2 ** 31 - 1, 8192) > 2 ** 35
 
 
 def test_norm_python_checks():

@@ -19,6 +19,8 @@ using pa::host::aligned;
 constexpr int kSms = 148;
 constexpr int kSmemPerSm = 208 * 1024;  // for rows in flight
 
+int32_t div_up(int32_t a, int32_t b) { return static_cast<int32_t>((static_cast<int64_t>(a) + b - 1) / b); }
+
 // The backward's blocks: teams of threads that own the channels 8 (or 16, 32) a thread, runs of rows, and tiles of
 // them with row_warps warps a row; as many rows in flight as shared memory holds.  `rows`, `chunks` and `teams` (all
 // that the workspace depends on) follow from the sizes alone.
@@ -35,8 +37,8 @@ BwdSplit split_bwd(int32_t total, int32_t hidden) {
   s.team_warps = (hidden + 256 * s.vecs - 1) / (256 * s.vecs);
   s.teams = 8 / s.team_warps;
   s.per_sm = s.vecs == 1 ? 16 / (s.teams * s.team_warps) : 1;  // by the kernels' registers
-  s.rows = std::max(1, (total + kSms * s.per_sm - 1) / (kSms * s.per_sm));
-  s.chunks = (total + s.rows - 1) / s.rows;
+  s.rows = std::max(1, div_up(total, kSms * s.per_sm));
+  s.chunks = div_up(total, s.rows);
   return s;
 }
 void split_bwd_rows(BwdSplit* s, int32_t hidden, int32_t row_bytes) {
@@ -120,12 +122,12 @@ FwdSplit split_fwd(int32_t total, int32_t hidden, int32_t row_bytes) {
   s.ring_offset = 12 * hidden;
   const int room = (kSmemPerSm - s.ring_offset) / row_bytes;  // rows
   const int most = pa::kNormFwdThreads / 32 / s.warps;
-  s.rows = (total + kSms - 1) / kSms;
+  s.rows = div_up(total, kSms);
   // rows for two groups of three to be worked on and for one on its way (with half as many groups the same time,
   // with a group for every row no better); more where there is room, and no more groups than rows
   s.groups = std::max(1, std::min({most, room * 2 / 3, s.rows}));
   s.stages = std::max(1, std::min(pa::kNormMaxStages, room / s.groups));
-  s.blocks = (total + s.rows - 1) / s.rows;
+  s.blocks = div_up(total, s.rows);
   return s;
 }
 

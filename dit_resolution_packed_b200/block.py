@@ -52,9 +52,15 @@ def declare(lib):
         fn.restype, fn.argtypes = res, args
 
 
+_lib = None
+
+
 def _library():
-    import dit_resolution_packed_b200 as pa
-    return pa.load_library()
+    global _lib
+    if _lib is None:
+        import dit_resolution_packed_b200 as pa
+        _lib = pa.load_library()
+    return _lib
 
 
 def _raise_on(rc, where):
@@ -65,17 +71,26 @@ def _raise_on(rc, where):
 
 def _handle(stream, like):
     """cudaStream_t of ``stream``, or of the current stream of the device that ``like`` lives on."""
-    import torch
-    if stream is None:
-        if not like.is_cuda:
-            return None  # the call refuses host memory
-        stream = torch.cuda.current_stream(like.device)
-    return stream.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if not like.is_cuda:
+        return None  # the call refuses host memory
+    global _current
+    if _current is None:
+        import torch
+        _current = torch._C._cuda_getCurrentRawStream  # what current_stream() wraps, at a tenth of its time
+    return _current(like.get_device())
+
+
+_current = None
+_HERE = contextlib.nullcontext()
 
 
 def _under(stream):
+    if stream is None:
+        return _HERE
     import torch
-    return torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
+    return torch.cuda.stream(stream)
 
 
 def _p(t):
@@ -87,9 +102,9 @@ def _check(dtype, shape, **tensors):
     for name, t in tensors.items():
         if t is None:
             continue
-        if t.dtype != dtype:
+        if t.dtype is not dtype:
             raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        if shape is not None and tuple(t.shape) != tuple(shape):
+        if shape is not None and t.shape != shape:
             raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
@@ -102,36 +117,37 @@ def _norm_desc(like, cu_seqlens, gate, post, w_post, residual_scale, pre, w_pre,
     if like.dim() != 2:
         raise ValueError("the residual stream must be [T, C]")
     T, C = like.shape
-    if like.dtype not in (torch.bfloat16, torch.float32):
+    f32, bf16 = torch.float32, torch.bfloat16
+    if like.dtype is not bf16 and like.dtype is not f32:
         raise TypeError(f"the residual stream must be bfloat16 or float32, got {like.dtype}")
     if post not in NORM_KINDS or pre not in NORM_KINDS:
         raise ValueError(f"post and pre must be one of {sorted(NORM_KINDS)}")
-    given = {"gate": gate, "scale": scale, "shift": shift, "w_post": w_post, "w_pre": w_pre}
-    types = {t.dtype for t in given.values() if t is not None}
-    if len(types) > 1 or not types <= {torch.bfloat16, torch.float32}:
-        raise TypeError("gate, scale, shift and the weights must be all bfloat16 or all float32")
-    B = 0
+    B = 1  # without cu_seqlens: one segment over all tokens, which nothing reads
     if cu_seqlens is not None:
         _check(torch.int32, None, cu_seqlens=cu_seqlens)
         B = cu_seqlens.numel() - 1
-    for name in ("gate", "scale", "shift"):
-        t = given[name]
+    kind, at, strides = None, [], []
+    for name, t in (("gate", gate), ("scale", scale), ("shift", shift), ("w_post", w_post), ("w_pre", w_pre)):
+        row = name[0] != "w"  # of an image, or one weight for all
         if t is None:
+            at.append(None)
+            if row:
+                strides.append(0)
             continue
-        if cu_seqlens is None:
-            raise ValueError(f"{name} needs cu_seqlens")
-        if tuple(t.shape) != (B, C) or (C > 1 and t.stride(1) != 1):
-            raise ValueError(f"{name} must be [B, C] with contiguous rows")
-    for name in ("w_post", "w_pre"):
-        t = given[name]
-        if t is not None and (tuple(t.shape) != (C,) or not t.is_contiguous()):
+        kind = kind or t.dtype
+        if t.dtype is not kind or (kind is not bf16 and kind is not f32):
+            raise TypeError("gate, scale, shift and the weights must be all bfloat16 or all float32")
+        if row:
+            if cu_seqlens is None:
+                raise ValueError(f"{name} needs cu_seqlens")
+            if t.shape != (B, C) or t.stride(1) != 1:
+                raise ValueError(f"{name} must be [B, C] with contiguous rows")
+            strides.append(t.stride(0))
+        elif t.shape != (C,) or t.stride(0) != 1:
             raise ValueError(f"{name} must be [C], contiguous")
-    if cu_seqlens is None:
-        B = 1  # one segment over all tokens: nothing reads it
-    stride = [t.stride(0) if t is not None else 0 for t in (gate, scale, shift)]
-    return BlockNormDesc(T, B, C, int(like.dtype == torch.float32), int(types == {torch.float32}), NORM_KINDS[post],
-                         NORM_KINDS[pre], residual_scale, eps, _p(cu_seqlens), _p(gate), _p(scale), _p(shift),
-                         *stride, _p(w_post), _p(w_pre))
+        at.append(t.data_ptr())
+    return BlockNormDesc(T, B, C, like.dtype is f32, kind is f32, NORM_KINDS[post], NORM_KINDS[pre], residual_scale, eps,
+                         _p(cu_seqlens), at[0], at[1], at[2], strides[0], strides[1], strides[2], at[3], at[4])
 
 
 def pa_block_norm_workspace_bytes(batch, total_tokens, hidden):
@@ -160,7 +176,7 @@ def block_norm_fwd(x, cu_seqlens=None, *, y=None, gate=None, post="none", w_post
     import torch
     with _under(stream):
         r = torch.empty_like(x) if y is not None else None
-        z = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device) if pre != "none" else None
+        z = torch.empty_like(x, dtype=torch.bfloat16) if pre != "none" else None
     rc = pa_block_norm_fwd(x, cu_seqlens, y, r, z, gate=gate, post=post, w_post=w_post, residual_scale=residual_scale,
                            pre=pre, w_pre=w_pre, scale=scale, shift=shift, eps=eps, stream=stream)
     _raise_on(rc, "pa_block_norm_fwd")
@@ -190,16 +206,14 @@ def block_norm_bwd(r, cu_seqlens=None, dr=None, dz=None, *, y=None, gate=None, p
     dy, dgate, dscale, dshift (fp32 [B, C]), dw_post, dw_pre (fp32 [C])."""
     import torch
     C = r.shape[1]
-    f32 = dict(dtype=torch.float32, device=r.device)
     with _under(stream):
         out = dict(dx=torch.empty_like(r), dy=torch.empty_like(y) if y is not None else None)
         for name, t in (("dgate", gate), ("dscale", scale), ("dshift", shift), ("dw_post", w_post), ("dw_pre", w_pre)):
-            out[name] = torch.empty(t.shape, **f32) if t is not None else None
+            out[name] = r.new_empty(t.shape, dtype=torch.float32) if t is not None else None
         ws = None
         if any(t is not None for t in (gate, scale, shift, w_post, w_pre)):
             B = cu_seqlens.numel() - 1 if cu_seqlens is not None else 1
-            ws = torch.empty(max(pa_block_norm_workspace_bytes(B, r.shape[0], C), 0), dtype=torch.uint8,
-                             device=r.device)
+            ws = r.new_empty(max(pa_block_norm_workspace_bytes(B, r.shape[0], C), 0), dtype=torch.uint8)
     rc = pa_block_norm_bwd(r, cu_seqlens, y, dr, dz, out["dx"], out["dy"], out["dgate"], out["dscale"], out["dshift"],
                            out["dw_post"], out["dw_pre"], ws, gate=gate, post=post, w_post=w_post,
                            residual_scale=residual_scale, pre=pre, w_pre=w_pre, scale=scale, shift=shift, eps=eps,
@@ -278,8 +292,8 @@ def qkv_rope_axes_fwd(x, w_qkv, pos, heads, head_dim, dims, theta=10000.0, inter
     import torch
     T = x.shape[0]
     with _under(stream):
-        q, k, v = (torch.empty(T, heads, head_dim, dtype=torch.bfloat16, device=x.device) for _ in range(3))
-        ws = torch.empty(max(pa_rope_axes_workspace_bytes(T, head_dim), 0), dtype=torch.uint8, device=x.device)
+        q, k, v = (x.new_empty((T, heads, head_dim)) for _ in range(3))
+        ws = x.new_empty(max(pa_rope_axes_workspace_bytes(T, head_dim), 0), dtype=torch.uint8)
     _raise_on(pa_qkv_rope_axes_fwd(x, w_qkv, pos, dims, theta, interleaved, q, k, v, ws, stream),
               "pa_qkv_rope_axes_fwd")
     return q, k, v
@@ -324,7 +338,7 @@ def pa_block_select(q, k, cu_seqlens, max_seqlen, density, min_blocks, idx, cnt,
     """C ``pa_block_select``: q, k bf16 [T, H, d]; idx int32 [H, rows, width], cnt int32 [H, rows] (written);
     workspace a byte tensor.  Returns the status code."""
     T, H, d, B = _pack(cu_seqlens, q=q, k=k)
-    width = _lists(idx, cnt, H, pa_block_rows(B, T))
+    width = _lists(idx, cnt, H, T // BLOCK_TOKENS + B)
     return _library().pa_block_select(_p(q), _p(k), _p(cu_seqlens), B, T, H, d, int(max_seqlen), float(density),
                                       int(min_blocks), width, _p(idx), _p(cnt), _p(workspace), workspace.numel(),
                                       _handle(stream, q))
@@ -337,13 +351,15 @@ def block_select(q, k, cu_seqlens, max_seqlen, density, min_blocks=1, stream=Non
     Returns idx int32 [H, rows, width] (increasing, -1 behind the list) and cnt int32 [H, rows]; block b of image s
     is row cu_seqlens[s] // 128 + s + b."""
     import torch
-    T, H, d, B = _pack(cu_seqlens, q=q, k=k)
+    T, H, d = q.shape
+    B = cu_seqlens.numel() - 1
     nb = max(1, -(-int(max_seqlen) // BLOCK_TOKENS))
     width = min(nb, max(int(min_blocks), math.ceil(density * nb)))
     with _under(stream):
-        idx = torch.empty(H, pa_block_rows(B, T), max(width, 1), dtype=torch.int32, device=q.device)
-        cnt = torch.empty(H, pa_block_rows(B, T), dtype=torch.int32, device=q.device)
-        ws = torch.empty(max(pa_block_select_workspace_bytes(B, T, H, d), 0), dtype=torch.uint8, device=q.device)
+        rows = T // BLOCK_TOKENS + B
+        idx = q.new_empty((H, rows, max(width, 1)), dtype=torch.int32)
+        cnt = q.new_empty((H, rows), dtype=torch.int32)
+        ws = q.new_empty(max(pa_block_select_workspace_bytes(B, T, H, d), 0), dtype=torch.uint8)
     _raise_on(pa_block_select(q, k, cu_seqlens, max_seqlen, density, min_blocks, idx, cnt, ws, stream),
               "pa_block_select")
     return idx, cnt
@@ -361,7 +377,7 @@ def pa_block_sparse_attn_fwd(q, k, v, cu_seqlens, max_seqlen, idx, cnt, scale, o
     import torch
     T, H, d, B = _pack(cu_seqlens, q=q, k=k, v=v, out=out)
     _check(torch.float32, (T, H), lse=lse)
-    width = _lists(idx, cnt, H, pa_block_rows(B, T))
+    width = _lists(idx, cnt, H, T // BLOCK_TOKENS + B)
     return _library().pa_block_sparse_attn_fwd(_p(q), _p(k), _p(v), _p(cu_seqlens), B, T, H, d, int(max_seqlen),
                                                _p(idx), _p(cnt), width, float(scale), _p(out), _p(lse), _p(workspace),
                                                workspace.numel(), _handle(stream, q))
@@ -371,7 +387,7 @@ def _sparse_workspace(q, cu_seqlens, max_seqlen, idx, backward):
     import torch
     T, H, d = q.shape
     n = pa_block_sparse_workspace_bytes(cu_seqlens.numel() - 1, T, H, d, max(int(max_seqlen), 0), idx.shape[2], backward)
-    return torch.empty(max(n, 0), dtype=torch.uint8, device=q.device)
+    return q.new_empty(max(n, 0), dtype=torch.uint8)
 
 
 def block_sparse_attn_fwd(q, k, v, cu_seqlens, max_seqlen, idx, cnt, scale=None, stream=None):
@@ -382,7 +398,7 @@ def block_sparse_attn_fwd(q, k, v, cu_seqlens, max_seqlen, idx, cnt, scale=None,
         scale = q.shape[-1] ** -0.5
     with _under(stream):
         out = torch.empty_like(q)
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+        lse = q.new_empty(q.shape[:2], dtype=torch.float32)
         ws = _sparse_workspace(q, cu_seqlens, max_seqlen, idx, False)
     _raise_on(pa_block_sparse_attn_fwd(q, k, v, cu_seqlens, max_seqlen, idx, cnt, scale, out, lse, ws, stream),
               "pa_block_sparse_attn_fwd")
@@ -396,7 +412,7 @@ def pa_block_sparse_attn_bwd(q, k, v, out, lse, dout, cu_seqlens, max_seqlen, id
     import torch
     T, H, d, B = _pack(cu_seqlens, q=q, k=k, v=v, out=out, dout=dout, dq=dq, dk=dk, dv=dv)
     _check(torch.float32, (T, H), lse=lse)
-    width = _lists(idx, cnt, H, pa_block_rows(B, T))
+    width = _lists(idx, cnt, H, T // BLOCK_TOKENS + B)
     return _library().pa_block_sparse_attn_bwd(_p(q), _p(k), _p(v), _p(out), _p(lse), _p(dout), _p(cu_seqlens), B, T, H,
                                                d, int(max_seqlen), _p(idx), _p(cnt), width, float(scale), _p(dq),
                                                _p(dk), _p(dv), _p(workspace), workspace.numel(), _handle(stream, q))

@@ -108,6 +108,7 @@ struct BwdParams {
   const int32_t* desc;    // [items][kBwdDescInts]: seg, beg, len, head, k0, query blocks
   const uint32_t* bits;   // [items][words] query blocks that name the key block
   int32_t words;
+  int32_t out32;          // dk and dv are 32-byte aligned: whole sectors per store
   const uint8_t* maps;    // [B][4] tensor maps: q, k, v, dout
 };
 constexpr int kBwdDescInts = 12;
@@ -181,20 +182,34 @@ __device__ __forceinline__ BwdItem bwd_decode_item(int32_t item, const BwdParams
   return w;
 }
 
-// kSparse: the item in the plan's descriptors.
-__device__ __forceinline__ BwdItem bwd_listed_item(int32_t item, const BwdParams& p) {
+// kSparse: the next item, looked up in three dependent reads (counter, order, the plan's descriptor) that the producer
+// spreads over the current item's last tiles, so that they do not stand between two items.
+struct BwdLookUp {
+  int32_t at, row;
   BwdItem w;
-  w.row = __ldg(p.order + item);
-  const int32_t* d = p.desc + static_cast<int64_t>(w.row) * kBwdDescInts;
-  w.seg = __ldg(d);
-  w.beg = __ldg(d + 1);
-  w.len = __ldg(d + 2);
-  w.head = __ldg(d + 3);
-  w.k0 = __ldg(d + 4);
-  w.nq = __ldg(d + 5);
-  w.id = item;
-  return w;
-}
+  __device__ __forceinline__ void read(int k, const BwdParams& p, int32_t n_items) {
+    if (k == 0) at = atomicAdd(p.next_item, 1);
+    if (k == 1) row = at < n_items ? __ldg(p.order + at) : -1;
+    if (k == 2) {
+      w.seg = -1;
+      if (row >= 0) {
+        const int4* d = reinterpret_cast<const int4*>(p.desc + static_cast<int64_t>(row) * kBwdDescInts);
+        const int4 a = __ldg(d), b = __ldg(d + 1);
+        w.seg = a.x;
+        w.beg = a.y;
+        w.len = a.z;
+        w.head = a.w;
+        w.k0 = b.x;
+        w.nq = b.y;
+        w.id = at;
+        w.row = row;
+      }
+    }
+  }
+  __device__ __forceinline__ void rest(int from, const BwdParams& p, int32_t n_items) {
+    for (int k = from; k < 3; ++k) read(k, p, n_items);
+  }
+};
 
 __device__ __forceinline__ void bwd_store_item(volatile int32_t* d, const BwdItem& w) {
   d[0] = w.seg; d[1] = w.beg; d[2] = w.len; d[3] = w.head; d[4] = w.k0; d[5] = w.nq; d[6] = w.row; d[7] = w.id;
@@ -235,29 +250,40 @@ __device__ __forceinline__ void bwd_producer(const BwdParams& p, uint8_t* smem, 
   bool kv_armed = false;
   uint32_t kv_armed_ph = 0, q_armed = 0, q_armed_ph = 0;
   bool ok = true;
+  BwdLookUp next;
+  int32_t mapped = -1;  // kSparse: segment whose tensor maps have been acquired
+  if constexpr (kSparse) next.rest(0, p, n_items);
   for (;;) {
     const int ss = sk & 1;
     const uint32_t sph = (sk >> 1) & 1u;
     ++sk;
     if (!(ok = mbar_wait(&bars->sched_empty[ss], sph ^ 1u, wc))) break;
-    const int32_t item = atomicAdd(p.next_item, 1);
     BwdItem w;
-    if (item < n_items) {
-      w = kSparse ? bwd_listed_item(item, p) : bwd_decode_item(item, p, n_sorted);
+    if constexpr (kSparse) {
+      w = next.w;
     } else {
-      w.seg = -1;
+      const int32_t item = atomicAdd(p.next_item, 1);
+      if (item < n_items) {
+        w = bwd_decode_item(item, p, n_sorted);
+      } else {
+        w.seg = -1;
+      }
     }
     bwd_store_item(bars->sched_item[ss], w);
     mbar_arrive(&bars->sched_full[ss]);
     if (w.seg < 0) break;
-    if (kSparse && w.nq == 0) continue;
+    if (kSparse && w.nq == 0) {
+      next.rest(0, p, n_items);
+      continue;
+    }
 
     const uint8_t* maps = p.maps + (kSparse ? static_cast<size_t>(w.seg) * 4 * 128 : 0);
     const void* mq = kSparse ? static_cast<const void*>(maps) : &p.tm_q;
     const void* mk = kSparse ? static_cast<const void*>(maps + 128) : &p.tm_k;
     const void* mv = kSparse ? static_cast<const void*>(maps + 256) : &p.tm_v;
     const void* mdo = kSparse ? static_cast<const void*>(maps + 384) : &p.tm_do;
-    if (kSparse) {
+    if (kSparse && w.seg != mapped) {
+      mapped = w.seg;
       fence_tmap_acquire(mq);
       fence_tmap_acquire(mk);
       fence_tmap_acquire(mv);
@@ -265,20 +291,15 @@ __device__ __forceinline__ void bwd_producer(const BwdParams& p, uint8_t* smem, 
     }
     const int32_t row0 = kSparse ? 0 : w.beg;  // of the segment, in the maps' coordinates
     const int32_t xcol = w.head * D;
-    if (!(ok = mbar_wait(&bars->kv_empty, (kv_round & 1u) ^ 1u, wc))) break;
-    mbar_arrive_expect_tx(&bars->kv_full, 2u * C::kTileBytes);
-    kv_armed = true;
-    kv_armed_ph = kv_round & 1u;
-    ++kv_round;
-#pragma unroll
-    for (int cb = 0; cb < C::kColBlocks; ++cb) {
-      tma_load_2d(smem + C::kOffK + cb * C::kBlockBytes, mk, xcol + cb * 64, row0 + w.k0, &bars->kv_full);
-      tma_load_2d(smem + C::kOffV + cb * C::kBlockBytes, mv, xcol + cb * 64, row0 + w.k0, &bars->kv_full);
-    }
     BwdQueryWalk<kSparse> walk(p, w);
-    for (int32_t i = 0; ok && i < w.nq; ++i) {
+    int looked = 0;
+    // the i-th query tile's Q and dO
+    auto load_queries = [&](int32_t i) -> bool {
       const int32_t y = row0 + walk.next(i) * 128;
-      if (!(ok = mbar_wait(&bars->qd_empty[qslot], qphase ^ 1u, wc))) break;
+      if constexpr (kSparse) {
+        if (i >= w.nq - 3) next.read(looked++, p, n_items);
+      }
+      if (!mbar_wait(&bars->qd_empty[qslot], qphase ^ 1u, wc)) return false;
       mbar_arrive_expect_tx(&bars->qd_full[qslot], 2u * C::kTileBytes);
       q_armed |= 1u << qslot;
       q_armed_ph = (q_armed_ph & ~(1u << qslot)) | (qphase << qslot);
@@ -293,8 +314,23 @@ __device__ __forceinline__ void bwd_producer(const BwdParams& p, uint8_t* smem, 
         qslot = 0;
         qphase ^= 1u;
       }
+      return true;
+    };
+    // short items: the first query tile comes while the previous item still works with its K and V
+    if (kSparse && !(ok = load_queries(0))) break;
+    if (!(ok = mbar_wait(&bars->kv_empty, (kv_round & 1u) ^ 1u, wc))) break;
+    mbar_arrive_expect_tx(&bars->kv_full, 2u * C::kTileBytes);
+    kv_armed = true;
+    kv_armed_ph = kv_round & 1u;
+    ++kv_round;
+#pragma unroll
+    for (int cb = 0; cb < C::kColBlocks; ++cb) {
+      tma_load_2d(smem + C::kOffK + cb * C::kBlockBytes, mk, xcol + cb * 64, row0 + w.k0, &bars->kv_full);
+      tma_load_2d(smem + C::kOffV + cb * C::kBlockBytes, mv, xcol + cb * 64, row0 + w.k0, &bars->kv_full);
     }
+    for (int32_t i = kSparse ? 1 : 0; ok && i < w.nq; ++i) ok = load_queries(i);
     if (!ok) break;
+    if constexpr (kSparse) next.rest(looked, p, n_items);
   }
   if (!ok) {
     // Let every copy this thread started land before the CTA can exit.
@@ -640,14 +676,18 @@ __device__ __forceinline__ void bwd_reduce_store(const BwdParams& p, BwdBars* ba
       PA_TMEM_LD32((is_k ? tDK : tDV) + 32 * c, a);
       tmem_wait_ld();
       uint4* dst = is_k ? dkp : dvp;
+      uint4 va[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        uint4 va;
-        va.x = pack_bf16x2(__uint_as_float(a[8 * u + 0]), __uint_as_float(a[8 * u + 1]));
-        va.y = pack_bf16x2(__uint_as_float(a[8 * u + 2]), __uint_as_float(a[8 * u + 3]));
-        va.z = pack_bf16x2(__uint_as_float(a[8 * u + 4]), __uint_as_float(a[8 * u + 5]));
-        va.w = pack_bf16x2(__uint_as_float(a[8 * u + 6]), __uint_as_float(a[8 * u + 7]));
-        if (key_ok) dst[c * 4 + u] = va;
+        va[u].x = pack_bf16x2(__uint_as_float(a[8 * u + 0]), __uint_as_float(a[8 * u + 1]));
+        va[u].y = pack_bf16x2(__uint_as_float(a[8 * u + 2]), __uint_as_float(a[8 * u + 3]));
+        va[u].z = pack_bf16x2(__uint_as_float(a[8 * u + 4]), __uint_as_float(a[8 * u + 5]));
+        va[u].w = pack_bf16x2(__uint_as_float(a[8 * u + 6]), __uint_as_float(a[8 * u + 7]));
+        if (!(kSparse && p.out32) && key_ok) dst[c * 4 + u] = va[u];
+      }
+      if (kSparse && p.out32 && key_ok) {
+        store_32b(dst + c * 4, va[0], va[1]);
+        store_32b(dst + c * 4 + 2, va[2], va[3]);
       }
     }
     tc_fence_before();

@@ -30,6 +30,7 @@ struct SparseFwdParams {
   float* lse;
   int32_t* status;
   int32_t heads, width;
+  int32_t out32;          // out is 32-byte aligned: whole sectors per store
   float scale_log2;
   uint64_t wait_limit_ns;
   int32_t err_timeout;
@@ -58,7 +59,8 @@ struct SparseItem {
   __device__ __forceinline__ int32_t cnt(int tile) const { return tile ? cnt1 : cnt0; }
 };
 
-__device__ __forceinline__ SparseItem sparse_item(const volatile int32_t* d) {
+template <class P>
+__device__ __forceinline__ SparseItem sparse_item(P d) {
   SparseItem w;
   w.seg = d[0];
   w.beg = d[1];
@@ -80,7 +82,7 @@ __device__ __forceinline__ int sparse_next(SparseBars* bars, uint32_t& sk, const
   const uint32_t sph = (sk >> 1) & 1u;
   ++sk;
   if (!mbar_wait(&bars->sched_full[ss], sph, wc)) return -2;
-  w = sparse_item(bars->sched_item[ss]);
+  w = sparse_item(static_cast<const volatile int32_t*>(bars->sched_item[ss]));
   return w.seg < 0 ? 0 : 1;
 }
 
@@ -110,23 +112,37 @@ __device__ __forceinline__ void sparse_producer(const SparseFwdParams& p, uint8_
     }
     return true;
   };
+  // The next item is looked up while the current one's last steps load (counter, order, descriptor and first step
+  // are four dependent reads of L2, a fifth of a short item's time when they stand between two items): look_up(k)
+  // does the k-th read.
+  int32_t at = 0, item = -1, d[kDescInts];
+  int2 first = make_int2(0, 0);
+  auto look_up = [&](int k) {
+    if (k == 0) at = atomicAdd(p.next_item, 1);
+    if (k == 1) item = at >= n_items ? -1 : p.order != nullptr ? __ldg(p.order + at) : at;
+    if (k == 2 && item >= 0) {
+      const int4* src = reinterpret_cast<const int4*>(p.desc + static_cast<int64_t>(item) * kDescInts);
+#pragma unroll
+      for (int i = 0; i < kDescInts / 4; ++i) {
+        const int4 v = __ldg(src + i);
+        d[4 * i] = v.x;
+        d[4 * i + 1] = v.y;
+        d[4 * i + 2] = v.z;
+        d[4 * i + 3] = v.w;
+      }
+    }
+    if (k == 3 && item >= 0) first = __ldg(p.steps + static_cast<int64_t>(item) * p.width);
+  };
+  for (int k = 0; k < 4; ++k) look_up(k);
+  int32_t mapped = -1;  // segment whose tensor maps have been acquired
   for (;;) {
+    while (item >= 0 && d[0] < 0) {  // rows of the work list that hold no item are passed over
+      for (int k = 0; k < 4; ++k) look_up(k);
+    }
     const int ss = sk & 1;
     const uint32_t sph = (sk >> 1) & 1u;
     ++sk;
     if (!(ok = mbar_wait(&bars->sched_empty[ss], sph ^ 1u, wc))) break;
-    int32_t item = -1;
-    const int32_t* d = nullptr;
-    for (;;) {  // rows of the work list that hold no item are passed over
-      const int32_t at = atomicAdd(p.next_item, 1);
-      if (at >= n_items) {
-        item = -1;
-        break;
-      }
-      item = p.order != nullptr ? __ldg(p.order + at) : at;
-      d = p.desc + static_cast<int64_t>(item) * kDescInts;
-      if (__ldg(d) >= 0) break;
-    }
     volatile int32_t* to = bars->sched_item[ss];
     if (item < 0) {
       to[0] = -1;
@@ -134,18 +150,25 @@ __device__ __forceinline__ void sparse_producer(const SparseFwdParams& p, uint8_
       break;
     }
 #pragma unroll
-    for (int i = 0; i < kDescInts; ++i) to[i] = __ldg(d + i);
-    const SparseItem w = sparse_item(to);
+    for (int i = 0; i < kDescInts; ++i) to[i] = d[i];
+    const SparseItem w = sparse_item(d);
     mbar_arrive(&bars->sched_full[ss]);
     const int32_t n = w.steps();
-    if (n == 0) continue;
-
+    if (n == 0) {
+      for (int k = 0; k < 4; ++k) look_up(k);
+      continue;
+    }
     const uint8_t* maps = p.maps + static_cast<size_t>(w.seg) * 3 * 128;
     const void *mq = maps, *mk = maps + 128, *mv = maps + 256;
-    fence_tmap_acquire(mq);
-    fence_tmap_acquire(mk);
-    fence_tmap_acquire(mv);
+    if (w.seg != mapped) {
+      fence_tmap_acquire(mq);
+      fence_tmap_acquire(mk);
+      fence_tmap_acquire(mv);
+      mapped = w.seg;
+    }
     const int32_t xcol = w.head * D;
+    const int2* steps = p.steps + static_cast<int64_t>(item) * p.width;
+    int2 cur = first;
     if (!(ok = mbar_wait(&bars->q_empty, (q_round & 1u) ^ 1u, wc))) break;
     mbar_arrive_expect_tx(&bars->q_full, (w.two ? 2u : 1u) * C::kTileBytes);
     q_armed = true;
@@ -158,13 +181,13 @@ __device__ __forceinline__ void sparse_producer(const SparseFwdParams& p, uint8_
         tma_load_2d(smem + C::kOffQ + C::kTileBytes + cb * C::kBlockBytes, mq, xcol + cb * 64, w.q0 + 128,
                     &bars->q_full);
     }
-    const int2* steps = p.steps + static_cast<int64_t>(item) * p.width;
-    int2 cur = __ldg(steps);
     if (w.cnt0 > 0 && !(ok = load_tile(mk, xcol, cur.x))) break;
     if (w.cnt1 > 0 && w.common == 0 && !(ok = load_tile(mk, xcol, cur.y))) break;
+    int looked = 0;
     for (int32_t j = 0; j < n; ++j) {
       const bool more = j + 1 < n;
       const int2 nxt = more ? __ldg(steps + j + 1) : cur;
+      if (j >= n - 4) look_up(looked++);
       if (j < w.cnt0) {
         if (!(ok = load_tile(mv, xcol, cur.x))) break;
         if (j + 1 < w.cnt0 && !(ok = load_tile(mk, xcol, nxt.x))) break;
@@ -176,6 +199,7 @@ __device__ __forceinline__ void sparse_producer(const SparseFwdParams& p, uint8_
       cur = nxt;
     }
     if (!ok) break;
+    for (; looked < 4; ++looked) look_up(looked);
   }
   if (!ok) {
     // Let every copy this thread started land before the CTA can exit.
@@ -345,14 +369,22 @@ __device__ __forceinline__ void sparse_softmax(const SparseFwdParams& p, SparseB
       uint32_t o[32];
       PA_TMEM_LD32(tO + cc * 32, o);
       tmem_wait_ld();
+      uint4 v[4];
 #pragma unroll
       for (int q4 = 0; q4 < 4; ++q4) {
-        uint4 v;
-        v.x = pack_bf16x2(__uint_as_float(o[q4 * 8 + 0]) * inv_l, __uint_as_float(o[q4 * 8 + 1]) * inv_l);
-        v.y = pack_bf16x2(__uint_as_float(o[q4 * 8 + 2]) * inv_l, __uint_as_float(o[q4 * 8 + 3]) * inv_l);
-        v.z = pack_bf16x2(__uint_as_float(o[q4 * 8 + 4]) * inv_l, __uint_as_float(o[q4 * 8 + 5]) * inv_l);
-        v.w = pack_bf16x2(__uint_as_float(o[q4 * 8 + 6]) * inv_l, __uint_as_float(o[q4 * 8 + 7]) * inv_l);
-        if (row_ok) dst[cc * 4 + q4] = v;
+        v[q4].x = pack_bf16x2(__uint_as_float(o[q4 * 8 + 0]) * inv_l, __uint_as_float(o[q4 * 8 + 1]) * inv_l);
+        v[q4].y = pack_bf16x2(__uint_as_float(o[q4 * 8 + 2]) * inv_l, __uint_as_float(o[q4 * 8 + 3]) * inv_l);
+        v[q4].z = pack_bf16x2(__uint_as_float(o[q4 * 8 + 4]) * inv_l, __uint_as_float(o[q4 * 8 + 5]) * inv_l);
+        v[q4].w = pack_bf16x2(__uint_as_float(o[q4 * 8 + 6]) * inv_l, __uint_as_float(o[q4 * 8 + 7]) * inv_l);
+      }
+      if (row_ok) {
+        if (p.out32) {
+          store_32b(dst + cc * 4, v[0], v[1]);
+          store_32b(dst + cc * 4 + 2, v[2], v[3]);
+        } else {
+#pragma unroll
+          for (int q4 = 0; q4 < 4; ++q4) dst[cc * 4 + q4] = v[q4];
+        }
       }
     }
     tc_fence_before();

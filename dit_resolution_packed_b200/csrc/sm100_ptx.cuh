@@ -428,6 +428,13 @@ __device__ __forceinline__ void tmem_ld128_pairs(uint32_t taddr, uint64_t (&v)[6
       : "memory");
 }
 
+// One 32-byte store (a whole sector; `addr` 32-byte aligned).
+__device__ __forceinline__ void store_32b(void* addr, const uint4& a, const uint4& b) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(addr), "r"(a.x), "r"(a.y), "r"(a.z),
+               "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+               : "memory");
+}
+
 // *addr += {a, b, c, d} (four fp32 reductions in one request, in L2; relaxed).
 __device__ __forceinline__ void red_add_v4_f32(float* addr, float a, float b, float c, float d) {
   asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(addr), "f"(a), "f"(b), "f"(c), "f"(d)

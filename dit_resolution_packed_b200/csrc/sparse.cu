@@ -73,6 +73,12 @@ int32_t keep_count(int32_t nb, double density, int32_t min_blocks) {
   return std::min(nb, std::max(min_blocks, static_cast<int32_t>(std::ceil(density * static_cast<double>(nb)))));
 }
 
+// Shared memory of select_topk_kernel: the group's query means, a chunk of key means, the warps' parts, the scores.
+size_t topk_smem(int32_t head_dim, int32_t nb) {
+  return 8 * (8 * static_cast<size_t>(head_dim) + 32 * (static_cast<size_t>(head_dim) + 2) + 8 * 8 * 32 +
+              8 * static_cast<size_t>(nb));
+}
+
 // Shared-memory limits of this file's kernels, once per device (the caller holds the library's lock).
 int ensure_kernels(int dev) {
   static bool ready[64] = {};
@@ -80,7 +86,7 @@ int ensure_kernels(int dev) {
   auto big = [](const void* f, int bytes) {
     return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
   };
-  const int topk = 8 * (8 * 128 + 32 * 129 + 8 * pa::kSelectMaxBlocks);
+  const int topk = static_cast<int>(topk_smem(128, pa::kSelectMaxBlocks));
   if (!big(reinterpret_cast<const void*>(pa::attn_sparse_fwd_kernel<64>), pa::FwdCfg<64>::kSmemBytes) ||
       !big(reinterpret_cast<const void*>(pa::attn_sparse_fwd_kernel<128>), pa::FwdCfg<128>::kSmemBytes) ||
       !big(reinterpret_cast<const void*>(pa::attn_bwd_kernel<64, true>), pa::BwdCfg<64>::kSmemBytes) ||
@@ -205,7 +211,7 @@ int pa_block_select(const void* q, const void* k, const int32_t* cu_seqlens, int
                            call.stream>>>(p);
   if ((rc = pa::host::launch_status()) != PA_OK) return rc;
   const dim3 grid(static_cast<unsigned>(total_tokens / 1024 + batch), heads);
-  const size_t smem = 8 * (8 * static_cast<size_t>(head_dim) + 32 * (static_cast<size_t>(head_dim) + 1) + 8 * nb);
+  const size_t smem = topk_smem(head_dim, nb);
   if (head_dim == 128)
     pa::select_topk_kernel<128><<<grid, 256, smem, call.stream>>>(p);
   else
@@ -272,6 +278,7 @@ int pa_block_sparse_attn_fwd(const void* q, const void* k, const void* v, const 
   f.status = call.status;
   f.heads = heads;
   f.width = width;
+  f.out32 = aligned(out, 32) ? 1 : 0;
   f.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   f.wait_limit_ns = call.wait_limit_ns;
   f.err_timeout = PA_ERR_TIMEOUT;
@@ -365,6 +372,7 @@ int pa_block_sparse_attn_bwd(const void* q, const void* k, const void* v, const 
   b.desc = p.desc;
   b.bits = p.bits;
   b.words = p.words;
+  b.out32 = aligned(dk, 32) && aligned(dv, 32) ? 1 : 0;
   b.maps = p.maps;
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(call.sms, items));
   if (head_dim == 128)

@@ -137,13 +137,18 @@ __device__ __forceinline__ uint64_t score_key(double s) {
   return (b >> 63) ? ~b : (b | (1ull << 63));
 }
 
-// One block per (group of 8 query blocks, head); warp w selects for query block w of the group.
+// One block per (group of 8 query blocks, head).  Scores: a chunk of 32 key blocks at a time, each warp an eighth of the
+// channels for all 8 x 32 pairs (a lane one key block and 8 sums, so a value read from shared memory serves 8
+// products), the warps' parts added in order; the next chunk's means come into registers meanwhile.  Then warp w
+// selects for query block w of the group.
 template <int D>
 __global__ void __launch_bounds__(256) select_topk_kernel(const __grid_constant__ SelectParams p) {
-  extern __shared__ double sm[];
-  double* qs = sm;                          // [8][D]
-  double* ks = qs + 8 * D;                  // [32][D + 1]: a chunk of key blocks (odd stride: no bank conflicts)
-  uint64_t* keys = reinterpret_cast<uint64_t*>(ks + 32 * (D + 1));  // [8][nb]
+  extern __shared__ __align__(16) double sm[];
+  constexpr int kRow = D + 2;  // of a key block's means: 16-byte aligned, and no bank conflicts across 32 rows
+  double* qs = sm;             // [8][D]
+  double* ks = qs + 8 * D;     // [32][kRow]
+  double* part = ks + 32 * kRow;  // [8 warps][8 query blocks][32]
+  uint64_t* keys = reinterpret_cast<uint64_t*>(part + 8 * 8 * 32);  // [8][nb]
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int h = blockIdx.y;
   const UnitAt u = unit_at(p.cu, p.batch, p.total, p.max_seqlen, blockIdx.x, 10);
@@ -153,35 +158,68 @@ __global__ void __launch_bounds__(256) select_topk_kernel(const __grid_constant_
   const int64_t row0 = (u.beg >> 7) + u.seg;  // of the segment's first block
   const double* qm = p.mean + (static_cast<int64_t>(h) * p.rows + row0) * D;
   const double* km = qm + static_cast<int64_t>(p.heads) * p.rows * D;
-  for (int i = threadIdx.x; i < nq * D; i += 256) qs[i] = qm[q0 * D + i];
-  uint64_t* mine = keys + static_cast<size_t>(w) * nb;
-  for (int k0 = 0; k0 < nb; k0 += 32) {
-    const int n = min(32, nb - k0);
-    __syncthreads();  // the last chunk's readers are done
-    for (int i = threadIdx.x; i < n * D; i += 256) ks[(i / D) * (D + 1) + i % D] = km[static_cast<int64_t>(k0) * D + i];
-    __syncthreads();
-    if (w < nq && lane < n) {
-      const double* a = qs + w * D;
-      const double* b = ks + lane * (D + 1);
-      double s0 = 0.0, s1 = 0.0, s2 = 0.0, s3 = 0.0;
-#pragma unroll 4
-      for (int c = 0; c < D; c += 4) {
-        s0 = fma(a[c], b[c], s0);
-        s1 = fma(a[c + 1], b[c + 1], s1);
-        s2 = fma(a[c + 2], b[c + 2], s2);
-        s3 = fma(a[c + 3], b[c + 3], s3);
-      }
-      mine[k0 + lane] = score_key((s0 + s1) + (s2 + s3));
+  for (int i = threadIdx.x; i < 8 * D; i += 256) qs[i] = i < nq * D ? qm[q0 * D + i] : 0.0;
+  constexpr int kPer = 32 * D / 512;  // pairs of means a thread brings
+  double2 next[kPer];
+  auto fetch = [&](int k0) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int at = (threadIdx.x + 256 * i) * 2;
+      next[i] = k0 * D + at < nb * D ? *reinterpret_cast<const double2*>(km + static_cast<int64_t>(k0) * D + at)
+                                     : make_double2(0.0, 0.0);
     }
+  };
+  fetch(0);
+  for (int k0 = 0; k0 < nb; k0 += 32) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int at = (threadIdx.x + 256 * i) * 2;
+      *reinterpret_cast<double2*>(ks + (at / D) * kRow + at % D) = next[i];
+    }
+    __syncthreads();
+    if (k0 + 32 < nb) fetch(k0 + 32);
+    double acc[8];
+#pragma unroll
+    for (int r = 0; r < 8; ++r) acc[r] = 0.0;
+#pragma unroll 4
+    for (int c = w * (D / 8); c < (w + 1) * (D / 8); c += 2) {
+      const double2 b = *reinterpret_cast<const double2*>(ks + lane * kRow + c);
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        const double2 a = *reinterpret_cast<const double2*>(qs + r * D + c);
+        acc[r] = fma(a.x, b.x, acc[r]);
+        acc[r] = fma(a.y, b.y, acc[r]);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < 8; ++r) part[(w * 8 + r) * 32 + lane] = acc[r];
+    __syncthreads();
+    double s = 0.0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s += part[(i * 8 + w) * 32 + lane];
+    if (k0 + lane < nb) keys[static_cast<size_t>(w) * nb + k0 + lane] = score_key(s);
   }
   __syncwarp();
   if (w >= nq) return;
+  const uint64_t* mine = keys + static_cast<size_t>(w) * nb;
   const int keep = min(nb, max(p.min_blocks, static_cast<int>(ceil(p.density * static_cast<double>(nb)))));
   // the largest threshold that at least `keep` scores reach, bit by bit from the top; done early when exactly
   // `keep` reach it
-  uint64_t bar = 0;
+  uint64_t all = ~0ull, any = 0;  // the scores' common leading bits need no count
+  for (int i = lane; i < nb; i += 32) {
+    all &= mine[i];
+    any |= mine[i];
+  }
+  const uint64_t differ =
+      (static_cast<uint64_t>(__reduce_or_sync(0xffffffffu, static_cast<uint32_t>(any >> 32)) ^
+                             __reduce_and_sync(0xffffffffu, static_cast<uint32_t>(all >> 32)))
+       << 32) |
+      (__reduce_or_sync(0xffffffffu, static_cast<uint32_t>(any)) ^
+       __reduce_and_sync(0xffffffffu, static_cast<uint32_t>(all)));
+  const int top = differ == 0 ? -1 : 63 - __clzll(static_cast<long long>(differ));
+  uint64_t bar = top == 63 ? 0 : mine[0] >> (top + 1) << (top + 1);
   int reached = nb;
-  for (int bit = 63; bit >= 0 && reached != keep; --bit) {
+  for (int bit = top; bit >= 0 && reached != keep; --bit) {
     const uint64_t cand = bar | (1ull << bit);
     int c = 0;
     for (int i = lane; i < nb; i += 32) c += mine[i] >= cand;

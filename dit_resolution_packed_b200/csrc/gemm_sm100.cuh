@@ -214,6 +214,8 @@ __device__ __forceinline__ void gemm_epilogue(const GemmParams& p, GemmBars* bar
   const uint32_t lane_base = static_cast<uint32_t>(r & ~31) << 16;
   uint32_t af_ph = 0;
   int local = 0;
+  // the table kernel may still run while the first tiles are multiplied (programmatic dependent launch)
+  if (kEpi == kEpiQkvAxes) pdl_wait_primary();
   for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++local) {
     const int buf = local & 1;
     const bool ok = mbar_wait(&bars->acc_full[buf], (af_ph >> buf) & 1u, wc);

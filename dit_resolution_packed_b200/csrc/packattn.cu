@@ -315,11 +315,26 @@ int launch_after_schedule(void (*kernel)(P), const P& params, int grid, size_t s
 }
 
 // Launches the projection GEMM (epilogue kEpi) on the persistent grid.
+// `overlap`: as a programmatic dependent launch behind the kernel that forms what only the epilogue reads.
 template <int kEpi>
-int launch_gemm(const pa::GemmParams& gp, int dev, cudaStream_t stream) {
+int launch_gemm(const pa::GemmParams& gp, int dev, cudaStream_t stream, bool overlap = false) {
   const int64_t tiles = ((static_cast<int64_t>(gp.M) + pa::kGemmBM - 1) / pa::kGemmBM) *
                         ((static_cast<int64_t>(gp.N) + pa::kGemmBN - 1) / pa::kGemmBN);
   const int grid = static_cast<int>(std::min<int64_t>(g_dev[dev].sms, tiles));
+  if (overlap) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(pa::kGemmThreads);
+    cfg.dynamicSmemBytes = pa::kGemmSmemBytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, pa::gemm_kernel<kEpi>, gp) != cudaSuccess) return PA_ERR_CUDA;
+    return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  }
   pa::gemm_kernel<kEpi><<<grid, pa::kGemmThreads, pa::kGemmSmemBytes, stream>>>(gp);
   return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
@@ -766,7 +781,7 @@ int pa_qkv_rope_axes_fwd(const void* x, const void* w_qkv, const float* pos, int
   gp.status = call.status;
   gp.wait_limit_ns = call.wait_limit_ns;
   gp.err_timeout = PA_ERR_TIMEOUT;
-  return launch_gemm<pa::kEpiQkvAxes>(gp, dev, call.stream);
+  return launch_gemm<pa::kEpiQkvAxes>(gp, dev, call.stream, true);
 }
 
 int pa_get_error(void* stream_handle) {

@@ -17,7 +17,7 @@ namespace pa {
 
 constexpr int kRopeThreads = 256;
 constexpr int kRopeMaxTokens = 32;
-constexpr int kRopeAhead = 4;  // units (of 32 bytes) that a thread has in flight
+constexpr int kRopeAhead = 3;  // units (of 32 bytes) that a thread has in flight, and about as many in all
 
 // The pairs of a head: frequency in turns per position, and axis (fits the constant bank of a launch).
 struct RopePairs {
@@ -35,11 +35,19 @@ struct RopeParams {
   RopePairs pairs;
 };
 
-__device__ __forceinline__ float2 rope_cos_sin(const RopePairs& pairs, const float* pos, int axes, int64_t token,
+// The launch's table of pairs as ordinary memory: its entries are read by lane (the constant bank would serve the 32
+// lanes one after the other).
+__device__ __forceinline__ const RopePairs* pairs_in_memory(const RopePairs& p) {
+  const RopePairs* q;
+  asm("mov.u64 %0, %1;" : "=l"(q) : "l"(&p));
+  return q;
+}
+
+__device__ __forceinline__ float2 rope_cos_sin(const RopePairs* pairs, const float* pos, int axes, int64_t token,
                                                int pair, float sign) {
-  const int a = pairs.axis[pair];
+  const int a = pairs->axis[pair];
   if (a < 0) return make_float2(1.f, 0.f);
-  const double t = static_cast<double>(pos[token * axes + a]) * pairs.turns[pair];
+  const double t = static_cast<double>(pos[token * axes + a]) * pairs->turns[pair];
   const float f = static_cast<float>(2.0 * (t - rint(t)));
   float s, c;
   sincospif(f, &s, &c);
@@ -114,7 +122,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_axes_kernel(const __grid_co
     if (!formed) {  // every thread passes here once, in its first turn
       formed = true;
       for (int i = threadIdx.x; i < tokens * half; i += kRopeThreads)
-        cs[i] = rope_cos_sin(p.pairs, p.pos, p.axes, token0 + i / half, i % half, p.sign);
+        cs[i] = rope_cos_sin(pairs_in_memory(p.pairs), p.pos, p.axes, token0 + i / half, i % half, p.sign);
       __syncthreads();
     }
 #pragma unroll
@@ -141,10 +149,11 @@ struct RopeTableParams {
 };
 
 __global__ void __launch_bounds__(256) rope_axes_table_kernel(const __grid_constant__ RopeTableParams p) {
+  pdl_launch_dependents();  // the projection reads the table in its epilogue only, behind its own wait
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   const int64_t token = i / p.half;
   if (token >= p.total) return;
-  p.table[i] = rope_cos_sin(p.pairs, p.pos, p.axes, token, static_cast<int>(i - token * p.half), 1.f);
+  p.table[i] = rope_cos_sin(pairs_in_memory(p.pairs), p.pos, p.axes, token, static_cast<int>(i - token * p.half), 1.f);
 }
 
 }  // namespace pa

@@ -213,7 +213,7 @@ int pa_block_norm_bwd(const pa_block_norm_desc* d, const void* r, const void* y,
   if (rc != PA_OK) return rc;
   const bool rows = d->total_tokens > 0;  // without tokens only the sums are memory that the call touches
   if (rows && ((d->pre == PA_NORM_NONE) != (dz == nullptr) || (!dz && !dr))) return PA_ERR_MODE;
-  if (rows && (y == nullptr) != (dy == nullptr)) return PA_ERR_MODE;
+  if (rows && ((y == nullptr) != (dy == nullptr) || (!y && !dz))) return PA_ERR_MODE;
   if (rows && !y && (d->post != PA_NORM_NONE || d->w_post || d->gate || d->residual_scale != 1.f)) return PA_ERR_MODE;
   if ((dgate && !d->gate) || (dscale && !d->scale) || (dshift && !d->shift) || (dw_post && !d->w_post) ||
       (dw_pre && !d->w_pre))

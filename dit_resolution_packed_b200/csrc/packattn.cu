@@ -117,7 +117,10 @@ StreamState* state_for(int device, cudaStream_t stream) {
 int ensure_status(StreamState* s) {
   if (s->status) return PA_OK;
   cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
-  if (cudaStreamIsCapturing(s->stream, &capture) != cudaSuccess) return PA_ERR_CUDA;
+  if (cudaStreamIsCapturing(s->stream, &capture) != cudaSuccess) {
+    cudaGetLastError();
+    return PA_ERR_CUDA;
+  }
   if (capture != cudaStreamCaptureStatusNone) {
     // A stream-ordered allocation made here would belong to the graph; the word has to outlive it.  So it is
     // allocated and cleared outside the capture, on a stream of its own.
@@ -386,7 +389,13 @@ Call::Call(int dev, void* stream_handle) : rc(PA_OK), stream(static_cast<cudaStr
     return;
   }
   if ((rc = ensure_device(dev)) != PA_OK) return;
-  StreamState* st = state_for(dev, stream);
+  StreamState* st = nullptr;
+  try {
+    st = state_for(dev, stream);
+  } catch (...) {  // no host memory: nothing is thrown across the C interface
+    rc = PA_ERR_CUDA;
+    return;
+  }
   if ((rc = ensure_status(st)) != PA_OK) return;
   sms = g_dev[dev].sms;
   status = st->status;

@@ -13,7 +13,9 @@
  * graphs, or two streams, that use different buffers never share one; the library itself holds only the
  * status word of the (device, stream) pair.  None of them synchronises or allocates on the device after
  * the first call on a stream, each may be captured into a CUDA graph, and each leaves the calling
- * thread's current device as it was.
+ * thread's current device as it was.  Device-side errors go to the status word of the stream that the call
+ * was made on (for a captured call: the capturing stream), to be read with pa_get_error.  After
+ * pa_release_workspace, graphs captured before must not be replayed (they hold that word's address).
  */
 #ifndef PACKATTN_BLOCK_H_
 #define PACKATTN_BLOCK_H_
@@ -89,7 +91,7 @@ PA_API int pa_block_norm_fwd(const pa_block_norm_desc* desc, const void* x, cons
  *     dgate[s] = sum over s's tokens of dr' u,  dscale[s] = sum of dz N_pre(r) w_pre,  dshift[s] = sum of dz,
  *     dw_post = sum over all tokens of dr' gate N_post(y),  dw_pre = sum of dz (1 + scale) N_pre(r).
  *   r            as the forward stored it (x when y is NULL).
- *   dz           NULL exactly when pre is NONE; with dz NULL, dr is given.
+ *   dz           NULL exactly when pre is NONE; with dz NULL, dr and y are given.
  *   dx           may be dr (in place).       dy   NULL exactly when y is.
  *   dgate, dscale, dshift   fp32 [batch, hidden], NULL if not wanted; a segment without tokens gets 0.
  *   dw_post, dw_pre         fp32 [hidden], NULL if not wanted.
@@ -125,6 +127,7 @@ typedef struct pa_rope_axes_desc {
  * pa_rope_axes -- rotate q and k [total_tokens, heads, head_dim] (bf16, contiguous, 16-byte aligned) on `stream`.
  *   inverse     0: the rotation; 1: its inverse, which is also its gradient (dq, dk in, gradients out).
  *   q_out, k_out may be q and k (in place); each rounded once.  k and k_out may both be NULL (q alone).
+ *   heads * head_dim below 2^19.  A position that is not finite makes its own axis' pairs NaN.
  */
 PA_API int pa_rope_axes(const void* q, const void* k, const float* pos, int32_t total_tokens, int32_t heads,
                         int32_t head_dim, const pa_rope_axes_desc* rope, int32_t inverse, void* q_out, void* k_out,
@@ -152,6 +155,8 @@ PA_API int pa_qkv_rope_axes_fwd(const void* x, const void* w_qkv, const float* p
  *   idx   device, int32, [heads, pa_block_rows, width]: key blocks of the row's segment, increasing.
  *   cnt   device, int32, [heads, pa_block_rows]: entries of the row's list, 0 .. width.  Entries past cnt, and
  *         rows that are no block, are not read.
+ * heads * head_dim is below 2^23.  Keys of a block that no list of a row names, other images' tokens and what
+ * lies behind a segment's last token have no influence on the row, whatever they hold (infinities, NaN).
  */
 PA_API int64_t pa_block_rows(int32_t batch, int32_t total_tokens);
 

@@ -74,6 +74,7 @@ def test_norm_fwd_refusals(lib, kw, code):
 @pytest.mark.parametrize("kw,code", [
     (dict(dz=None), pa.PA_ERR_MODE), (dict(pre=0), pa.PA_ERR_MODE), (dict(pre=0, dz=None, dr=None), pa.PA_ERR_MODE),
     (dict(y=16), pa.PA_ERR_MODE), (dict(dy=16), pa.PA_ERR_MODE), (dict(r=None), pa.PA_ERR_NULL),
+    (dict(pre=0, dz=None), pa.PA_ERR_MODE),
     (dict(dx=None), pa.PA_ERR_NULL), (dict(dx=20), pa.PA_ERR_ALIGN),
     (dict(sums=(16, None, None, None, None)), pa.PA_ERR_MODE),
     (dict(sums=(None, None, None, None, 16)), pa.PA_ERR_MODE),

@@ -301,7 +301,7 @@ struct NormFwdParams {
 // neighbours of either: fp32 values are then read and written 16 bytes a lane without bank conflicts (8 neighbours a
 // lane would meet every bank twice), bf16 values 8 bytes a lane.
 template <bool kF32>
-__device__ __forceinline__ Pairs8 load_halves(const void* p, size_t c, int h) {
+__device__ __forceinline__ Pairs8 load_halves(const void* p, int64_t c, int h) {
   Pairs8 v;
   if (kF32) {
     const float* s = static_cast<const float*>(p) + c;
@@ -409,9 +409,11 @@ __global__ void __launch_bounds__(kNormFwdThreads, 1) block_norm_fwd_kernel(cons
   constexpr int kStep = kW * 256;
   // f(c, h) for the lane's channels, sweep by sweep
   auto sweep = [&](auto f) {
+    int base = warp * 256;
 #pragma unroll 4
-    for (int base = warp * 256; base < C; base += kStep) {
-      const int h = min(128, (C - base) >> 1);
+    for (; base + 256 <= C; base += kStep) f(base + lane * 4, 128);
+    if (base < C) {  // the row's short end
+      const int h = (C - base) >> 1;
       if (lane * 4 < h) f(base + lane * 4, h);
     }
   };
@@ -562,11 +564,7 @@ struct BackRow {
     uint64_t t[14];
 #pragma unroll
     for (int i = 0; i < 14; ++i) t[i] = 0;
-#pragma unroll 2
-    for (int base = from; base < C; base += step) {
-      const int h = min(128, (C - base) >> 1);
-      if (lane * 4 >= h) continue;
-      const int c = base + lane * 4;
+    auto add = [&](int c, int h) {
       Pairs8 d, f, e, q, g;
       if (kFront) {
         d = load_halves<kF32>(r, c, h);
@@ -608,6 +606,13 @@ struct BackRow {
           }
         }
       }
+    };
+    int base = from;
+#pragma unroll(kBehind ? 1 : 2)
+    for (; base + 256 <= C; base += step) add(base + lane * 4, 128);
+    if (base < C) {  // the row's short end
+      const int h = (C - base) >> 1;
+      if (lane * 4 < h) add(base + lane * 4, h);
     }
     float v[14];
 #pragma unroll
@@ -760,9 +765,11 @@ __global__ void __launch_bounds__(256, kG == 1 ? 2 : 1)
     }
     __syncthreads();
     for (int r = team; r < n; r += bp.teams) {
-      mbar_wait(ring.full + ring.stage_of(p, r), ring.phase_of(p, r), wc);
+      // (with a first phase, a thread of this block has waited for each row, and the barrier above stands between)
+      if (!front && !normed) mbar_wait(ring.full + ring.stage_of(p, r), ring.phase_of(p, r), wc);
       const uint8_t* src = ring.row(p, r);
-      const size_t at = static_cast<size_t>(row + r) * C;
+      uint8_t* dx = static_cast<uint8_t*>(p.r) + (row + r) * static_cast<int64_t>(wide);
+      uint8_t* dy = static_cast<uint8_t*>(p.z) + (row + r) * static_cast<int64_t>(narrow);
       const float4 sr = scalars[r][0], sy = scalars[r][1];
       const uint64_t mr2 = pair_of(-sr.x, -sr.x), r2 = pair_of(sr.y, sr.y), n0 = pair_of(-sr.z, -sr.z),
                      n1 = pair_of(-sr.w, -sr.w);
@@ -786,7 +793,7 @@ __global__ void __launch_bounds__(256, kG == 1 ? 2 : 1)
         Pairs8 t;
 #pragma unroll
         for (int i = 0; i < 4; ++i) t.p[i] = f2_mul(res2, d.p[i]);
-        store_halves<kF32>(p.r, at + col[k], half[k], t);
+        store_halves<kF32>(dx, col[k], half[k], t);
         if (!join) continue;
         Pairs8 y = load_halves<false>(src + br + bz + bd, col[k], half[k]);
         if (normed) {
@@ -803,7 +810,7 @@ __global__ void __launch_bounds__(256, kG == 1 ? 2 : 1)
             d.p[i] = f2_mul(d.p[i], g[k].p[i]);
           }
         }
-        store_halves<false>(p.z, at + col[k], half[k], d);
+        store_halves<false>(dy, col[k], half[k], d);
       }
     }
     __syncthreads();  // the tile's stages, scalars and factors are free

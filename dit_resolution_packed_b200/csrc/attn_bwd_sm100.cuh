@@ -738,6 +738,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_kernel(const __grid_c
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
   const WaitCtl wc{&bars->abort_flag, p.status, p.wait_limit_ns, p.err_timeout};
+  if (kSparse) pdl_wait_primary();  // launched behind the kernel that forms D and clears dq's accumulator
   const int32_t n_items = p.counts[0];
   const int32_t n_sorted = p.counts[1];
   if (warp < 8) {

@@ -297,12 +297,13 @@ int pa_block_norm_bwd(const pa_block_norm_desc* d, const void* r, const void* y,
   sp.use = (dgate || dw_post ? 1 : 0) | (dscale || dw_pre ? 2 : 0) | (dshift ? 4 : 0);
   // 64 segments fill the GPU; with fewer, a segment's slots are read in parallel
   if (p.batch > 64)
-    pa::block_norm_sum_kernel<<<dim3(p.batch, (p.hidden + 4 * pa::kNormSumThreads - 1) / (4 * pa::kNormSumThreads)),
-                                pa::kNormSumThreads, 0, call.stream>>>(sp);
+    rc = pa::host::launch_behind(pa::block_norm_sum_kernel,
+                                 dim3(p.batch, (p.hidden + 4 * pa::kNormSumThreads - 1) / (4 * pa::kNormSumThreads)),
+                                 pa::kNormSumThreads, 0, call.stream, sp);
   else
-    pa::block_norm_sum_long_kernel<<<dim3(p.batch, (p.hidden + 127) / 128), pa::kNormSumLongThreads, 0, call.stream>>>(
-        sp);
-  if ((rc = pa::host::launch_status()) != PA_OK || !weights) return rc;
+    rc = pa::host::launch_behind(pa::block_norm_sum_long_kernel, dim3(p.batch, (p.hidden + 127) / 128),
+                                 pa::kNormSumLongThreads, 0, call.stream, sp);
+  if (rc != PA_OK || !weights) return rc;
   pa::NormWeightParams wp;
   std::memset(&wp, 0, sizeof(wp));
   wp.batch = p.batch;
@@ -315,8 +316,7 @@ int pa_block_norm_bwd(const pa_block_norm_desc* d, const void* r, const void* y,
   wp.scale_stride = d->scale_stride;
   wp.dw_post = dw_post;
   wp.dw_pre = dw_pre;
-  pa::block_norm_weight_kernel<<<dim3((p.hidden + 31) / 32, 2), 256, 0, call.stream>>>(wp);
-  return pa::host::launch_status();
+  return pa::host::launch_behind(pa::block_norm_weight_kernel, dim3((p.hidden + 31) / 32, 2), 256, 0, call.stream, wp);
 }
 
 }  // extern "C"

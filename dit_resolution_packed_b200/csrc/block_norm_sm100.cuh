@@ -887,6 +887,7 @@ __device__ __forceinline__ void put_sum(const NormSumParams& p, int32_t s, int k
 // after slot (a short image has one or two).
 constexpr int kNormSumThreads = 256;
 __global__ void __launch_bounds__(kNormSumThreads) block_norm_sum_kernel(const __grid_constant__ NormSumParams p) {
+  pdl_wait_primary();
   const int col = (blockIdx.y * kNormSumThreads + threadIdx.x) * 4;
   if (col >= p.hidden) return;
   const int32_t s = blockIdx.x;
@@ -903,6 +904,7 @@ __global__ void __launch_bounds__(kNormSumThreads) block_norm_sum_kernel(const _
 // sums are added in order.
 constexpr int kNormSumLongThreads = 1024;
 __global__ void __launch_bounds__(kNormSumLongThreads) block_norm_sum_long_kernel(const __grid_constant__ NormSumParams p) {
+  pdl_wait_primary();
   __shared__ float4 acc[3][32][32];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int col = blockIdx.y * 128 + lane * 4;
@@ -940,6 +942,7 @@ struct NormWeightParams {
 // dw_post = sum_s gate[s] A[s], dw_pre = sum_s (1 + scale[s]) B[s]: one block per 32 channels and weight, its
 // 8 warps taking the segments 8 apart.
 __global__ void __launch_bounds__(256) block_norm_weight_kernel(const __grid_constant__ NormWeightParams p) {
+  pdl_wait_primary();
   __shared__ float acc[8][32];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int col = blockIdx.x * 32 + lane;

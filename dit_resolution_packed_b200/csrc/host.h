@@ -50,5 +50,22 @@ int launch_rope_table(const float* pos, int32_t total, int32_t head_dim, const p
 
 inline int launch_status() { return cudaGetLastError() == cudaSuccess ? 0 : -8; }
 
+// Launches a kernel that begins with griddepcontrol.wait as a programmatic dependent of the one before it in the
+// stream: its blocks are placed, and what it does before that wait is done, while that one's last blocks run.
+template <class P>
+int launch_behind(void (*kernel)(P), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, const P& params) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, params) == cudaSuccess ? launch_status() : -8;
+}
+
 }  // namespace host
 }  // namespace pa

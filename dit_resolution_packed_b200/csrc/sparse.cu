@@ -212,11 +212,8 @@ int pa_block_select(const void* q, const void* k, const int32_t* cu_seqlens, int
   if ((rc = pa::host::launch_status()) != PA_OK) return rc;
   const dim3 grid(static_cast<unsigned>(total_tokens / 1024 + batch), heads);
   const size_t smem = topk_smem(head_dim, nb);
-  if (head_dim == 128)
-    pa::select_topk_kernel<128><<<grid, 256, smem, call.stream>>>(p);
-  else
-    pa::select_topk_kernel<64><<<grid, 256, smem, call.stream>>>(p);
-  return pa::host::launch_status();
+  return pa::host::launch_behind(head_dim == 128 ? pa::select_topk_kernel<128> : pa::select_topk_kernel<64>, grid, 256, smem,
+                                 call.stream, p);
 }
 
 int64_t pa_block_sparse_workspace_bytes(int32_t batch, int32_t total_tokens, int32_t heads, int32_t head_dim,
@@ -261,10 +258,9 @@ int pa_block_sparse_attn_fwd(const void* q, const void* k, const void* v, const 
   if (p.sorted && cudaMemsetAsync(ws, 0, L.cleared, call.stream) != cudaSuccess) return PA_ERR_CUDA;
   pa::sparse_plan_fwd_kernel<<<warps4(items), 128, 0, call.stream>>>(p);
   if ((rc = pa::host::launch_status()) != PA_OK) return rc;
-  if (p.sorted) {
-    pa::sparse_order_kernel<<<order_blocks(items), 256, 0, call.stream>>>(p);
-    if ((rc = pa::host::launch_status()) != PA_OK) return rc;
-  }
+  if (p.sorted && (rc = pa::host::launch_behind(pa::sparse_order_kernel, order_blocks(items), 256, 0, call.stream, p)) !=
+                      PA_OK)
+    return rc;
   pa::SparseFwdParams f;
   std::memset(&f, 0, sizeof(f));
   f.counts = p.counts;
@@ -282,19 +278,10 @@ int pa_block_sparse_attn_fwd(const void* q, const void* k, const void* v, const 
   f.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   f.wait_limit_ns = call.wait_limit_ns;
   f.err_timeout = PA_ERR_TIMEOUT;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(call.sms, items)));
-  cfg.blockDim = dim3(pa::kFwdThreads);
-  cfg.dynamicSmemBytes = head_dim == 128 ? pa::FwdCfg<128>::kSmemBytes : pa::FwdCfg<64>::kSmemBytes;
-  cfg.stream = call.stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = head_dim == 128 ? cudaLaunchKernelEx(&cfg, pa::attn_sparse_fwd_kernel<128>, f)
-                                        : cudaLaunchKernelEx(&cfg, pa::attn_sparse_fwd_kernel<64>, f);
-  return e == cudaSuccess ? pa::host::launch_status() : PA_ERR_CUDA;
+  return pa::host::launch_behind(head_dim == 128 ? pa::attn_sparse_fwd_kernel<128> : pa::attn_sparse_fwd_kernel<64>,
+                                 static_cast<unsigned>(std::min<int64_t>(call.sms, items)), pa::kFwdThreads,
+                                 head_dim == 128 ? pa::FwdCfg<128>::kSmemBytes : pa::FwdCfg<64>::kSmemBytes, call.stream,
+                                 f);
 }
 
 int pa_block_sparse_attn_bwd(const void* q, const void* k, const void* v, const void* out, const float* lse,
@@ -334,10 +321,9 @@ int pa_block_sparse_attn_bwd(const void* q, const void* k, const void* v, const 
   if (cudaMemsetAsync(ws, 0, L.cleared, call.stream) != cudaSuccess) return PA_ERR_CUDA;
   pa::sparse_mark_kernel<<<warps4(items), 128, 0, call.stream>>>(p);
   if ((rc = pa::host::launch_status()) != PA_OK) return rc;
-  pa::sparse_plan_bwd_kernel<<<warps4(items), 128, 0, call.stream>>>(p);
-  if ((rc = pa::host::launch_status()) != PA_OK) return rc;
-  pa::sparse_order_kernel<<<order_blocks(items), 256, 0, call.stream>>>(p);
-  if ((rc = pa::host::launch_status()) != PA_OK) return rc;
+  if ((rc = pa::host::launch_behind(pa::sparse_plan_bwd_kernel, warps4(items), 128, 0, call.stream, p)) != PA_OK ||
+      (rc = pa::host::launch_behind(pa::sparse_order_kernel, order_blocks(items), 256, 0, call.stream, p)) != PA_OK)
+    return rc;
 
   float* lse2 = reinterpret_cast<float*>(ws + L.lse2);
   float* delta = reinterpret_cast<float*>(ws + L.delta);
@@ -375,11 +361,11 @@ int pa_block_sparse_attn_bwd(const void* q, const void* k, const void* v, const 
   b.out32 = aligned(dk, 32) && aligned(dv, 32) ? 1 : 0;
   b.maps = p.maps;
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(call.sms, items));
-  if (head_dim == 128)
-    pa::attn_bwd_kernel<128, true><<<grid, pa::kBwdThreads, pa::BwdCfg<128>::kSmemBytes, call.stream>>>(b);
-  else
-    pa::attn_bwd_kernel<64, true><<<grid, pa::kBwdThreads, pa::BwdCfg<64>::kSmemBytes, call.stream>>>(b);
-  if ((rc = pa::host::launch_status()) != PA_OK) return rc;
+  void (*kernel)(pa::BwdParams) = head_dim == 128 ? pa::attn_bwd_kernel<128, true> : pa::attn_bwd_kernel<64, true>;
+  if ((rc = pa::host::launch_behind(kernel, grid, pa::kBwdThreads,
+                                    head_dim == 128 ? pa::BwdCfg<128>::kSmemBytes : pa::BwdCfg<64>::kSmemBytes,
+                                    call.stream, b)) != PA_OK)
+    return rc;
 
   const unsigned conv = static_cast<unsigned>(((static_cast<int64_t>(total_tokens) + 31) / 32) * heads);
   auto convert = head_dim == 128 ? pa::bwd_dq_convert_kernel<128> : pa::bwd_dq_convert_kernel<64>;

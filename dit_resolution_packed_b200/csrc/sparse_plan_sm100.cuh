@@ -151,6 +151,7 @@ __global__ void __launch_bounds__(256) select_topk_kernel(const __grid_constant_
   uint64_t* keys = reinterpret_cast<uint64_t*>(part + 8 * 8 * 32);  // [8][nb]
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int h = blockIdx.y;
+  pdl_wait_primary();
   const UnitAt u = unit_at(p.cu, p.batch, p.total, p.max_seqlen, blockIdx.x, 10);
   if (!u.valid) return;
   const int nb = (u.len + 127) >> 7;
@@ -424,6 +425,7 @@ __global__ void __launch_bounds__(128) sparse_mark_kernel(const __grid_constant_
 // Backward, second: one warp per (head, key block) counts the query blocks that name it.
 __global__ void __launch_bounds__(128) sparse_plan_bwd_kernel(const __grid_constant__ SparsePlanParams p) {
   const int lane = threadIdx.x & 31;
+  pdl_wait_primary();
   const int64_t item = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
   if (item >= p.rows * p.heads) return;
   const int32_t h = static_cast<int32_t>(item / p.rows);
@@ -452,6 +454,7 @@ __global__ void __launch_bounds__(256) sparse_order_kernel(const __grid_constant
   __shared__ int32_t start[kSparseBuckets];
   __shared__ int32_t warp_sum_s[8];
   pdl_launch_dependents();
+  pdl_wait_primary();
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   int32_t v[4], local = 0;
 #pragma unroll

@@ -47,9 +47,10 @@ void split_bwd_rows(BwdSplit* s, int32_t hidden, int32_t row_bytes) {
   const int warps = s->teams * s->team_warps;
   s->stages = std::min(pa::kNormMaxBwdStages,
                        std::max(1, (kSmemPerSm / s->per_sm - s->ring_offset) / std::max(1, row_bytes)));
-  // as few warps a row as keep three quarters of the block's warps at work on a tile's rows
+  // as few warps a row as keep three quarters of the block's warps at work on a tile's rows, and never more than the
+  // block has: a group's barrier counts all its warps
   s->row_warps = 1;
-  while (s->row_warps < warps && 4 * s->row_warps * std::min(warps / s->row_warps, s->stages) < 3 * warps)
+  while (2 * s->row_warps <= warps && 4 * s->row_warps * std::min(warps / s->row_warps, s->stages) < 3 * warps)
     s->row_warps *= 2;
   s->tile = std::max(1, std::min({warps / s->row_warps, s->stages, pa::kNormMaxTile}));
 }

@@ -156,3 +156,49 @@ def test_merged_steps_and_the_ring_order():
         taken, uses = consumer(steps, common, len(l0), len(l1), slots=3)
         assert taken == producer(steps, common, len(l0), len(l1))
         assert len(uses) == 2 * (len(l0) + len(l1))
+
+
+# ---------------------------------------------------------------- splitting rules of the norms (csrc/block_norm.cu)
+
+SMEM_PER_SM = 208 * 1024
+SMEM_PER_BLOCK = 227 * 1024 - 8 * 1024  # the device's limit less the kernels' static shared memory
+
+
+def split_fwd(hidden, row_bytes, rows):
+    warps = 1 if hidden <= 2048 else 2 if hidden <= 4096 else 4
+    room = (SMEM_PER_SM - 12 * hidden) // row_bytes
+    groups = max(1, min(24 // warps, room * 2 // 3, rows))
+    stages = max(1, min(8, room // groups))
+    return warps, groups, stages, 12 * hidden + groups * stages * row_bytes
+
+
+def split_bwd(hidden, row_bytes):
+    vecs = 1 if hidden <= 2048 else 2 if hidden <= 4096 else 4
+    team_warps = (hidden + 256 * vecs - 1) // (256 * vecs)
+    teams = 8 // team_warps
+    per_sm = 16 // (teams * team_warps) if vecs == 1 else 1
+    stages = min(24, max(1, (SMEM_PER_SM // per_sm - 8 * hidden) // row_bytes))
+    warps, row_warps = teams * team_warps, 1
+    while 2 * row_warps <= warps and 4 * row_warps * min(warps // row_warps, stages) < 3 * warps:
+        row_warps *= 2
+    tile = max(1, min(warps // row_warps, stages, 12))
+    return dict(vecs=vecs, team_warps=team_warps, teams=teams, per_sm=per_sm, stages=stages, warps=warps,
+                row_warps=row_warps, tile=tile, smem=8 * hidden + stages * row_bytes)
+
+
+def test_norm_splits_fit_for_every_width():
+    for hidden in range(8, 8193, 8):
+        for wide in (2, 4):
+            for row_bytes in (wide * hidden, (wide + 2) * hidden):
+                for rows in (1, 5, 1000):
+                    warps, groups, stages, smem = split_fwd(hidden, row_bytes, rows)
+                    assert groups * warps <= 24 and groups * stages <= 8 * 24 and smem <= SMEM_PER_BLOCK
+                    assert groups <= 24 // warps and (warps == 1 or groups <= 15)  # a named barrier each
+                    assert groups * 8 <= groups * warps * 32  # threads that initialise the barriers
+            for row_bytes in (wide * hidden, (wide + 2) * hidden, (2 * wide + 2) * hidden, (2 * wide + 4) * hidden):
+                s = split_bwd(hidden, row_bytes)
+                assert s["team_warps"] * 256 * s["vecs"] >= hidden and 1 <= s["warps"] <= 8
+                assert s["row_warps"] <= s["warps"], "a group's barrier would count warps that the block does not have"
+                assert s["tile"] * s["row_warps"] <= s["warps"] and s["tile"] <= s["stages"]
+                assert s["smem"] <= SMEM_PER_BLOCK and s["stages"] <= s["warps"] * 32
+                assert s["per_sm"] * (s["smem"] + 8 * 1024) <= 227 * 1024 + 4 * 1024 * s["per_sm"] or s["stages"] == 1

@@ -108,7 +108,7 @@ struct BwdParams {
   const int32_t* desc;    // [items][kBwdDescInts]: seg, beg, len, head, k0, query blocks
   const uint32_t* bits;   // [items][words] query blocks that name the key block
   int32_t words;
-  int32_t out32;          // dk and dv are 32-byte aligned: whole sectors per store
+  int32_t out32;          // dk and dv are 32-byte aligned: whole sectors per store (sparse, 26 images: 3 % less)
   const uint8_t* maps;    // [B][4] tensor maps: q, k, v, dout
 };
 constexpr int kBwdDescInts = 12;

@@ -12,6 +12,10 @@
 // Unshared steps move 4 tiles of 128 d 2 bytes per two score tiles, twice the dense kernel's; from L2, which holds
 // a head's K and V.  A tile without keys writes zeros and lse = -infinity and takes part in nothing else.
 //
+// 16384 tokens, 24 heads, d = 128, an eighth of the blocks (random lists): 400 us, 1030 TFLOP/s of the products that the
+// lists ask for; the same with lists that both tiles share 10 % less.  Items are taken head by head (plan kernels), or
+// the loads cost 50 us more.
+//
 // Warps as in the dense kernel: 0-3 and 4-7 softmax and epilogue of tiles 0 and 1, 8 TMA producer, 9 MMA issuer.
 #pragma once
 #include "attn_fwd_sm100.cuh"
@@ -30,7 +34,7 @@ struct SparseFwdParams {
   float* lse;
   int32_t* status;
   int32_t heads, width;
-  int32_t out32;          // out is 32-byte aligned: whole sectors per store
+  int32_t out32;          // out is 32-byte aligned: whole sectors per store (the case above: 27 us less than 16 bytes)
   float scale_log2;
   uint64_t wait_limit_ns;
   int32_t err_timeout;

@@ -22,7 +22,8 @@ constexpr int kSmemPerSm = 208 * 1024;  // for rows in flight
 int32_t div_up(int32_t a, int32_t b) { return static_cast<int32_t>((static_cast<int64_t>(a) + b - 1) / b); }
 
 // The backward's blocks: teams of threads that own the channels 8 (or 16, 32) a thread, runs of rows, and tiles of
-// them with row_warps warps a row; as many rows in flight as shared memory holds.  `rows`, `chunks` and `teams` (all
+// them with row_warps warps a row; as many rows in flight as shared memory holds.  A thread owns more channels only
+// where 8 warps of 8 do not cover a row.  `rows`, `chunks` and `teams` (all
 // that the workspace depends on) follow from the sizes alone.
 struct BwdSplit {
   int32_t vecs, team_warps, teams, per_sm, rows, chunks;
@@ -48,7 +49,8 @@ void split_bwd_rows(BwdSplit* s, int32_t hidden, int32_t row_bytes) {
   s->stages = std::min(pa::kNormMaxBwdStages,
                        std::max(1, (kSmemPerSm / s->per_sm - s->ring_offset) / std::max(1, row_bytes)));
   // as few warps a row as keep three quarters of the block's warps at work on a tile's rows, and never more than the
-  // block has: a group's barrier counts all its warps
+  // block has: a group's barrier counts all its warps.  Measured by this rule, with one and with all warps a row, us:
+  // 16384 x 2048 110, 112, 110; 8192 x 4096 111, 122, 110; 4096 x 8192 132, 169, 132; 1152 and 1536 channels alike.
   s->row_warps = 1;
   while (2 * s->row_warps <= warps && 4 * s->row_warps * std::min(warps / s->row_warps, s->stages) < 3 * warps)
     s->row_warps *= 2;
@@ -111,6 +113,14 @@ int64_t part_floats(int32_t batch, int32_t hidden, const BwdSplit& s) {
 int64_t sum_floats(int32_t batch, int32_t hidden) { return 2 * static_cast<int64_t>(std::max(batch, 1)) * hidden; }
 
 // The forward's blocks: one per SM, groups of `warps` warps, each with a ring of rows behind the factors.
+// Warps a row: what a row costs whatever its width (shuffles, barriers) is paid by each of its warps, against which
+// long rows leave too few in shared memory for one warp each.  Measured with 1, 2 and 4 warps, bf16 / fp32 residual, us:
+//     16384 x 1536   42.3 / 58.5   45.2 / 57.9    63.6 / 73.2
+//     16384 x 2304   60.7 / 83.2   62.9 / 82.2    74.7 / 89.7
+//     16384 x 2560   68.2 / 93.7   66.9 / 90.1    76.4 / 97.5
+//      8192 x 3584   57.0 / 85.2   52.7 / 77.3    55.8 / 74.4
+//      8192 x 4096   70.1 / 93.0   63.5 / 85.5    59.6 / 81.1
+//      4096 x 8192    138 / 237     106 / 174     84.1 / 118
 struct FwdSplit {
   int32_t warps, groups, rows, blocks, stages, row_bytes, ring_offset;
   int threads() const { return warps * groups * 32; }
@@ -118,7 +128,7 @@ struct FwdSplit {
 };
 FwdSplit split_fwd(int32_t total, int32_t hidden, int32_t row_bytes) {
   FwdSplit s;
-  s.warps = hidden <= 2048 ? 1 : hidden <= 4096 ? 2 : 4;
+  s.warps = hidden <= 2304 ? 1 : hidden < 4096 ? 2 : 4;
   s.row_bytes = row_bytes;
   s.ring_offset = 12 * hidden;
   const int room = (kSmemPerSm - s.ring_offset) / row_bytes;  // rows
@@ -296,8 +306,10 @@ int pa_block_norm_bwd(const pa_block_norm_desc* d, const void* r, const void* y,
   sp.dscale = dscale;
   sp.dshift = dshift;
   sp.use = (dgate || dw_post ? 1 : 0) | (dscale || dw_pre ? 2 : 0) | (dshift ? 4 : 0);
-  // 64 segments fill the GPU; with fewer, a segment's slots are read in parallel
-  if (p.batch > 64)
+  // Some 40 segments fill the GPU; with fewer, a segment's slots are read in parallel.  The whole backward of
+  // 65536 x 1152 by one and the other: 3 segments 224 and 195 us, 16 201 and 194, 32 197.5 and 196, 48 197.5 and 200,
+  // 256 196 and 229, 2048 220 and 488.
+  if (p.batch > 40)
     rc = pa::host::launch_behind(pa::block_norm_sum_kernel,
                                  dim3(p.batch, (p.hidden + 4 * pa::kNormSumThreads - 1) / (4 * pa::kNormSumThreads)),
                                  pa::kNormSumThreads, 0, call.stream, sp);

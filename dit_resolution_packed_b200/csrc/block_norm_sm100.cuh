@@ -288,7 +288,7 @@ struct RunCursor {
 //
 // What bounds it once the loads run ahead is the number of instructions: at HBM's rate an SM has about 25 for a
 // channel of a bf16 join, and shuffles, exchanges and barriers cost the same whether a warp holds 256 channels or
-// 2048.  So one warp takes a whole row (kW of them above 2048 channels), and everything lives in shared memory: the
+// 2048.  So one warp takes a whole row (kW of them where rows are long), and everything lives in shared memory: the
 // row's tensors as they arrived, r over x once it is formed, and the segment's factors for all warps of the block.
 // A block (one per SM) takes a run of rows; its groups take them in turn, each with a ring of its own.
 struct NormFwdParams {

@@ -165,7 +165,7 @@ SMEM_PER_BLOCK = 227 * 1024 - 8 * 1024  # the device's limit less the kernels' s
 
 
 def split_fwd(hidden, row_bytes, rows):
-    warps = 1 if hidden <= 2048 else 2 if hidden <= 4096 else 4
+    warps = 1 if hidden <= 2304 else 2 if hidden < 4096 else 4
     room = (SMEM_PER_SM - 12 * hidden) // row_bytes
     groups = max(1, min(24 // warps, room * 2 // 3, rows))
     stages = max(1, min(8, room // groups))

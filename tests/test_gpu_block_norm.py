@@ -141,7 +141,7 @@ LENS = [3, 0, 130, 1, 64, 0]
 
 
 @pytest.mark.parametrize("f32", [False, True])
-@pytest.mark.parametrize("C", [520, 1152, 1536, 1800, 2304, 2560, 3080, 3584, 4096, 5120, 5128, 6144, 6152, 7168, 7176])
+@pytest.mark.parametrize("C", [520, 1152, 1536, 1800, 2304, 2312, 2560, 3080, 3584, 4088, 4096, 5120, 5128, 6144, 6152, 7168, 7176])
 def test_channels_of_every_split(cuda_device, C, f32):
     """Every number of warps that a row, a team and a block can have, with all four tensors in the rows."""
     _run(cuda_device, _case([70, 9], C, f32, 14), "layer", "layer")

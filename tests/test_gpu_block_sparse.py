@@ -125,6 +125,18 @@ def test_select_ties_nan_and_infinity(cuda_device):
         assert np.array_equal(cnt.cpu().numpy(), rc) and np.array_equal(idx.cpu().numpy(), ri)
 
 
+@pytest.mark.parametrize("lq,lk", [(-131, 0), (0, -131), (119, -100), (-60, 60), (119, 119)])
+def test_select_over_the_types_whole_range(cuda_device, lq, lk):
+    """Subnormal values and the largest: products down to 2^-260 and up to 2^254, which 64 bits hold exactly scaled."""
+    lens, H, d = [1500, 130], 3, 128
+    q, k, _, _, cu, longest = _inputs(lens, H, d, 23)
+    q, k = (torch.from_numpy(np.ldexp(x.double().numpy(), e)).to(torch.bfloat16) for x, e in ((q, lq), (k, lk)))
+    assert torch.isfinite(q).all() and torch.isfinite(k).all() and (q != 0).any() and (k != 0).any()
+    idx, cnt = pa.block_select(q.to(cuda_device), k.to(cuda_device), cu.to(cuda_device), longest, 0.4, 1)
+    ri, rc = ob.block_select(q, k, cu.numpy(), 0.4, 1, idx.shape[2])
+    assert np.array_equal(cnt.cpu().numpy(), rc) and np.array_equal(idx.cpu().numpy(), ri)
+
+
 def test_select_many_blocks_and_wider_tables(cuda_device):
     """A segment of 300 blocks (several words of each structure), max_seqlen above the longest, 40 short images."""
     for lens, H, d, density in (([128 * 300 - 5], 2, 64, 0.1), ([40] * 40 + [2000], 25, 64, 0.5)):

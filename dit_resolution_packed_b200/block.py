@@ -8,7 +8,6 @@ they may be freed or captured into a graph like any other tensor of that stream.
 import contextlib
 import ctypes
 import math
-import math
 
 NORM_KINDS = {"none": 0, "layer": 1, "rms": 2}
 

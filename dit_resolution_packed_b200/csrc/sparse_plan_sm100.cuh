@@ -280,18 +280,21 @@ struct SparsePlanParams {
   int32_t err_cu, err_max, err_blocks;
 };
 
-// The segment's tensor maps: the templates with base and row extent moved, so that a tile's rows past the segment
-// read zeros and nothing of a neighbouring image (whatever it holds) enters a product.
-__device__ __forceinline__ void write_maps(const SparsePlanParams& p, const UnitAt& u, int lane) {
-  if (lane < p.n_maps) {
-    uint8_t* dst = p.maps + (static_cast<size_t>(u.seg) * p.n_maps + lane) * 128;
-    const uint4* src = reinterpret_cast<const uint4*>(&p.tmpl[lane]);
+// The tensor maps of segment `seg`: the templates with base and row extent moved, so that a tile's rows past the
+// segment read zeros and nothing of a neighbouring image (whatever it holds) enters a product.  Warp `seg` of a plan
+// writes them (a work list has at least a row per segment), not the one that finds the segment's first unit: with
+// cu_seqlens that decrease, that row may be found to be another segment's, and later units of this one still exist.
+__device__ __forceinline__ void write_maps(const SparsePlanParams& p, int64_t seg, int lane) {
+  if (seg >= p.batch || lane >= p.n_maps) return;
+  const int32_t beg = __ldg(p.cu + seg), end = __ldg(p.cu + seg + 1);
+  if (beg < 0 || end <= beg || end > p.total) return;  // no units
+  uint8_t* dst = p.maps + (static_cast<size_t>(seg) * p.n_maps + lane) * 128;
+  const uint4* src = reinterpret_cast<const uint4*>(&p.tmpl[lane]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) reinterpret_cast<uint4*>(dst)[i] = src[i];
-    tmap_replace_address(dst, static_cast<const uint8_t*>(p.base[lane]) + static_cast<uint64_t>(u.beg) * p.row_bytes);
-    tmap_replace_dim1(dst, static_cast<uint32_t>(u.len));
-    fence_tmap_release();
-  }
+  for (int i = 0; i < 8; ++i) reinterpret_cast<uint4*>(dst)[i] = src[i];
+  tmap_replace_address(dst, static_cast<const uint8_t*>(p.base[lane]) + static_cast<uint64_t>(beg) * p.row_bytes);
+  tmap_replace_dim1(dst, static_cast<uint32_t>(end - beg));
+  fence_tmap_release();
 }
 
 // Length of a block's list, 0 (and the status recorded) if it is not an increasing list of the segment's blocks.
@@ -338,6 +341,7 @@ __global__ void __launch_bounds__(128) sparse_plan_fwd_kernel(const __grid_const
       p.counts[2] = 0;
     }
   }
+  write_maps(p, item, lane);
   if (item >= p.units * p.heads) return;
   const int32_t h = static_cast<int32_t>(item / p.units);
   const UnitAt u = unit_at(p.cu, p.batch, p.total, p.max_seqlen, item - h * p.units, 8);
@@ -349,7 +353,6 @@ __global__ void __launch_bounds__(128) sparse_plan_fwd_kernel(const __grid_const
     }
     return;
   }
-  if (h == 0 && u.unit == 0) write_maps(p, u, lane);
   const int32_t nb = (u.len + 127) >> 7;
   const bool two = u.unit * 256 + 128 < u.len;
   const int64_t at0 = static_cast<int64_t>(h) * p.rows + (u.beg >> 7) + u.seg + 2 * u.unit;
@@ -408,11 +411,11 @@ __global__ void __launch_bounds__(128) sparse_mark_kernel(const __grid_constant_
   const int lane = threadIdx.x & 31;
   const int64_t item = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
   if (blockIdx.x == 0) check_pack(p.cu, p.batch, p.total, p.max_seqlen, p.status, p.err_cu, p.err_max);
+  write_maps(p, item, lane);
   if (item >= p.rows * p.heads) return;
   const int32_t h = static_cast<int32_t>(item / p.rows);
   const UnitAt u = unit_at(p.cu, p.batch, p.total, p.max_seqlen, item - h * p.rows, 7);
   if (!u.valid) return;
-  if (h == 0 && u.unit == 0) write_maps(p, u, lane);
   const int32_t nb = (u.len + 127) >> 7;
   const int32_t n = checked_list(p, item, nb, lane);
   const int32_t* list = p.idx + item * p.width;

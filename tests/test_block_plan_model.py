@@ -67,6 +67,26 @@ def test_bad_packs_stay_inside_the_tables():
                     assert 0 <= (cu[s] >> 7) + s + blk < (total >> 7) + batch
 
 
+def test_bad_packs_have_a_map_for_every_unit():
+    """Tensor maps are written for segment s by warp s of a plan, whichever segment that warp's own row is found to be."""
+    def mapped(cu, total, warps):
+        return {s for s in range(warps) if s < len(cu) - 1 and cu[s] >= 0 and cu[s] < cu[s + 1] <= total}
+
+    rng = random.Random(13)
+    packs = [[0, 5000, 300, 6000]]  # the first units of the last segment are found to be the first segment's
+    packs += [[rng.randint(-3000, 8000) for _ in range(rng.randint(2, 11))] for _ in range(2000)]
+    late = False
+    for cu in packs:
+        total = 6000
+        for log2 in (7, 8):
+            rows = (total >> log2) + len(cu) - 1
+            found = [unit_at(cu, total, total, r, log2) for r in range(rows)]
+            have = mapped(cu, total, rows)
+            assert all(u[0] in have for u in found if u)
+            late |= any(u and (u[0], 0) not in found for u in found)
+    assert late
+
+
 def merge(l0, l1):
     """(steps as pairs with None, shared steps): common blocks first, then the rest side by side."""
     both = [v for v in l0 if v in l1]

@@ -285,6 +285,29 @@ def test_bad_lists_and_packs_are_recorded(cuda_device):
     both(pa.PA_OK)
 
 
+@pytest.mark.parametrize("bad", [[0, 5000, 300, 6000], [0, 3000, 2000, 2500, 1000, 6000], [0, 6000, 0, 6000], [0, 0, -5, 6000]])
+def test_packs_that_decrease_are_recorded(cuda_device, bad):
+    """Segments that overlap, of which some blocks' rows are found to be another segment's; into fresh workspaces."""
+    H, d = 2, 64
+    q, k, v, dout, cu, longest = (t.to(cuda_device) if torch.is_tensor(t) else t for t in _inputs([6000], H, d, 36))
+    rows = ob.table_rows(len(bad) - 1, 6000)
+    idx = torch.arange(3, dtype=torch.int32, device=cuda_device).repeat(H, rows, 1)
+    cnt = torch.full((H, rows), 3, dtype=torch.int32, device=cuda_device)
+    wrong = torch.tensor(bad, dtype=torch.int32, device=cuda_device)
+    out, lse = torch.zeros_like(q), torch.zeros((6000, H), device=cuda_device)
+    for backward in (0, 1):
+        n = pa.pa_block_sparse_workspace_bytes(len(bad) - 1, 6000, H, d, longest, 3, backward)
+        ws = torch.zeros(n, dtype=torch.uint8, device=cuda_device)
+        if backward:
+            g = [torch.empty_like(q) for _ in range(3)]
+            assert pa.pa_block_sparse_attn_bwd(q, k, v, out, lse, dout, wrong, longest, idx, cnt, 0.1, *g, ws) == pa.PA_OK
+        else:
+            assert pa.pa_block_sparse_attn_fwd(q, k, v, wrong, longest, idx, cnt, 0.1, out, lse, ws) == pa.PA_OK
+        assert pa.pa_get_error() == pa.PA_ERR_CU_SEQLENS
+    pa.block_select(q, k, wrong, longest, 0.3)
+    assert pa.pa_get_error() == pa.PA_ERR_CU_SEQLENS
+
+
 def test_no_tokens(cuda_device):
     cu = torch.zeros(3, dtype=torch.int32, device=cuda_device)
     q = torch.empty(0, 2, 64, dtype=torch.bfloat16, device=cuda_device)

@@ -155,6 +155,10 @@ struct GroupLink {
   }
 };
 
+// 1 / deviation of a variance that its roundings may have left below 0.  A NaN stays one (a maximum would make it 0,
+// and the row finite but for the channel that holds it): a row with a NaN, and for a layer norm with an infinity, is NaN.
+__device__ __forceinline__ float rstd_of(float var, float eps) { return rsqrtf((var < 0.f ? 0.f : var) + eps); }
+
 // The row's mean and 1 / deviation from its warps' moments, spread over the lanes by `exchange` (one warp: its own).
 __device__ __forceinline__ void merge_moments(float wm, float wq, float n, const GroupLink& link, float inv_c, int kind,
                                               float eps, float& mean, float& rstd) {
@@ -175,7 +179,7 @@ __device__ __forceinline__ void merge_moments(float wm, float wq, float n, const
   } else {
     mean = wm;
   }
-  rstd = rsqrtf(fmaxf(wq * inv_c, 0.f) + eps);
+  rstd = rstd_of(wq * inv_c, eps);
 }
 
 // The segment of a token, by a 32-way search of the warp: the last s in [0, batch) with cu[s] <= t (0 if none).
@@ -628,14 +632,14 @@ struct BackRow {
         delta = v[0] * inv_c;
         mean_r = pr + delta;
       }
-      rstd_r = rsqrtf(fmaxf(v[1] * inv_c - delta * delta, 0.f) + p.eps);
+      rstd_r = rstd_of(v[1] * inv_c - delta * delta, p.eps);
       c0 = p.pre == 1 ? v[2] * inv_c : 0.f;
       c1 = rstd_r * (v[3] - delta * v[2]) * inv_c;
     }
     out[0] = make_float4(mean_r, rstd_r, c0, c1);
     if (kBehind) {
       const float shift = kLayerBehind ? v[9] * inv_c : 0.f;
-      const float rstd_y = rsqrtf(fmaxf(v[4] * inv_c - shift * shift, 0.f) + p.eps);
+      const float rstd_y = rstd_of(v[4] * inv_c - shift * shift, p.eps);
       const float k = rstd_r * c1;
       const float sum_he = kFront ? v[5] + rstd_r * (v[6] - c0 * v[7] - k * (v[8] - delta * v[7])) : v[5];
       float e0 = 0.f, sum_h = 0.f;

@@ -1,0 +1,86 @@
+"""Infinities and NaN in the block operators: they reach what the formulas say they reach, and nothing else.
+
+The oracle says where an output is NaN; no tolerance enters.  Everything a NaN does not reach is compared bit by bit
+with the same call on finite inputs.
+"""
+import numpy as np
+import pytest
+import torch
+
+import dit_resolution_packed_b200 as pa
+from oracle import block as ob
+
+pytestmark = pytest.mark.gpu
+NAN, INF = float("nan"), float("inf")
+SUMS = ("dgate", "dscale", "dshift", "dw_post", "dw_pre")
+
+
+def _inputs(lens, C, f32, seed):
+    g = torch.Generator().manual_seed(seed)
+    wide = torch.float32 if f32 else torch.bfloat16
+    T, B = sum(lens), len(lens)
+    rn = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    t = dict(cu=torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32), x=rn(T, C).to(wide),
+             y=rn(T, C).to(torch.bfloat16), dr=rn(T, C).to(wide), dz=rn(T, C).to(torch.bfloat16))
+    m = (0.3 * rn(3, B, C)).to(wide)
+    t["gate"], t["scale"], t["shift"] = m[0].clone(), m[1].clone(), m[2].clone()
+    t["w_post"], t["w_pre"] = ((1 + 0.2 * rn(C)).to(wide) for _ in range(2))
+    return t
+
+
+def _run(dev, t, post, pre):
+    """(r, z, gradients) on the GPU, with the oracle's of the stored r."""
+    d = {k: v.to(dev) for k, v in t.items()}
+    how = dict(y=d["y"], gate=d["gate"], post=post, w_post=d["w_post"], pre=pre, w_pre=d["w_pre"], scale=d["scale"],
+               shift=d["shift"])
+    r, z = pa.block_norm_fwd(d["x"], d["cu"], **how)
+    out = pa.block_norm_bwd(r, d["cu"], d["dr"], d["dz"], **how)
+    assert pa.pa_get_error() == pa.PA_OK
+    cu = t["cu"].numpy()
+    with np.errstate(invalid="ignore", over="ignore"):
+        ref = ob.block_norm_bwd(r, cu, t["dr"], t["dz"], y=t["y"], gate=t["gate"], post=post, w_post=t["w_post"],
+                                pre=pre, w_pre=t["w_pre"], scale=t["scale"], shift=t["shift"])
+        ref["r"] = ob.join(t["x"], cu, t["y"], t["gate"], post, t["w_post"], 1.0)
+        ref["z"] = ob.front(r, cu, pre, t["w_pre"], t["scale"], t["shift"])
+    return dict(out, r=r, z=z), ref
+
+
+def _same_nans(got, ref, names, what):
+    for name in names:
+        assert np.array_equal(torch.isnan(got[name].float()).cpu().numpy(), np.isnan(ref[name])), f"{what}: {name}"
+
+
+# one, two and four warps a row forward; one team of each width backward
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("C", [72, 512, 2560, 4096])
+@pytest.mark.parametrize("post,pre", [("rms", "rms"), ("rms", "layer"), ("layer", "rms"), ("layer", "layer")])
+@pytest.mark.parametrize("where", ["x", "y", "dr", "dz"])
+def test_a_nan_reaches_its_row(cuda_device, where, post, pre, C, f32):
+    t = _inputs([40, 30], C, f32, 1)
+    clean, _ = _run(cuda_device, t, post, pre)
+    row, channel = 57, C - 3
+    t[where][row, channel] = NAN
+    got, ref = _run(cuda_device, t, post, pre)
+    _same_nans(got, ref, ("r", "z", "dx", "dy") + SUMS, f"NaN in {where}")
+    keep = torch.arange(70, device=cuda_device) != row
+    for name in ("r", "z", "dx", "dy"):
+        assert torch.equal(got[name][keep], clean[name][keep]), name
+    for name in ("dgate", "dscale", "dshift"):
+        assert torch.equal(got[name][0], clean[name][0]), name
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("C", [72, 512, 2560, 4096])
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+@pytest.mark.parametrize("channel", [0, -1])  # inside and behind the channels that a row's pivot is taken from
+def test_an_infinity_reaches_its_row(cuda_device, channel, kind, C, f32):
+    """Forward: a layer norm's whole row is NaN; an rms norm's is 0, and NaN where the infinity stands."""
+    t = _inputs([40, 30], C, f32, 2)
+    for where in ("x", "y"):
+        s = dict(t, **{where: t[where].clone()})
+        s[where][7, channel] = -INF
+        got, ref = _run(cuda_device, s, kind, kind)
+        _same_nans(got, ref, ("r", "z"), f"infinity in {where}")
+        name = "z" if where == "x" else "r"
+        nan = np.isnan(ref[name][7])
+        assert nan.all() if kind == "layer" else nan.sum() == 1

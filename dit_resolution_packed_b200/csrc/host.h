@@ -42,9 +42,10 @@ bool encode_rows(CUtensorMap* m, const void* base, int32_t rows, int32_t heads, 
 // Tensor map of a bf16 row-major [outer, inner] matrix, box {64, box_outer}, 128-byte swizzle.
 bool encode_matrix(CUtensorMap* m, const void* base, int64_t inner, int64_t outer, uint32_t box_outer);
 
-// Positions with several axes (rope_axes.cu): PA_OK or why a description is refused; the (cos, sin) of every
-// token and pair into `table`.
+// Positions with several axes (rope_axes.cu): PA_OK or why a description is refused; the pairs of a head that belong
+// to an axis; the (cos, sin) of every token and pair into `table`.
 int check_rope_axes(const pa_rope_axes_desc* rope, int32_t head_dim);
+int rope_turned(const pa_rope_axes_desc* rope);
 int launch_rope_table(const float* pos, int32_t total, int32_t head_dim, const pa_rope_axes_desc* rope, void* table,
                       cudaStream_t stream);
 

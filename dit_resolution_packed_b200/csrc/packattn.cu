@@ -787,6 +787,7 @@ int pa_qkv_rope_axes_fwd(const void* x, const void* w_qkv, const float* pos, int
   gp.head_dim = head_dim;
   gp.rope = static_cast<const float2*>(workspace);
   gp.interleaved = rope->interleaved;
+  gp.turned = pa::host::rope_turned(rope);
   gp.status = call.status;
   gp.wait_limit_ns = call.wait_limit_ns;
   gp.err_timeout = PA_ERR_TIMEOUT;

@@ -23,6 +23,7 @@ pa::RopePairs pairs_of(const pa_rope_axes_desc* r) {
       out.axis[p] = static_cast<int8_t>(a);
       out.turns[p] = std::pow(r->theta[a], -2.0 * i / r->dims[a]) / 6.283185307179586476925286766559;
     }
+  out.turned = p;
   for (; p < 64; ++p) out.axis[p] = -1;
   return out;
 }
@@ -42,6 +43,12 @@ int check_rope_axes(const pa_rope_axes_desc* r, int32_t head_dim) {
     sum += r->dims[a];
   }
   return sum <= head_dim ? PA_OK : PA_ERR_SHAPE;
+}
+
+int rope_turned(const pa_rope_axes_desc* rope) {
+  int pairs = 0;
+  for (int a = 0; a < rope->axes; ++a) pairs += rope->dims[a] / 2;
+  return pairs;
 }
 
 int launch_rope_table(const float* pos, int32_t total, int32_t head_dim, const pa_rope_axes_desc* rope, void* table,
@@ -102,10 +109,11 @@ int pa_rope_axes(const void* q, const void* k, const float* pos, int32_t total_t
   p.tokens = static_cast<int32_t>(std::max<int64_t>(
       1, std::min<int64_t>({pa::kRopeAhead * pa::kRopeThreads / per_token, fill, pa::kRopeMaxTokens})));
   const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(total_tokens) + p.tokens - 1) / p.tokens);
-  if (rope->interleaved)
-    pa::rope_axes_kernel<true><<<grid, pa::kRopeThreads, 0, call.stream>>>(p);
-  else
-    pa::rope_axes_kernel<false><<<grid, pa::kRopeThreads, 0, call.stream>>>(p);
+  const bool part = p.pairs.turned < head_dim / 2;
+  void (*kernel)(pa::RopeParams) =
+      rope->interleaved ? (part ? pa::rope_axes_kernel<true, true> : pa::rope_axes_kernel<true, false>)
+                        : (part ? pa::rope_axes_kernel<false, true> : pa::rope_axes_kernel<false, false>);
+  kernel<<<grid, pa::kRopeThreads, 0, call.stream>>>(p);
   return pa::host::launch_status();
 }
 

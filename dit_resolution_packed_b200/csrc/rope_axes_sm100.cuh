@@ -23,6 +23,7 @@ constexpr int kRopeAhead = 3;  // units (of 32 bytes) that a thread has in fligh
 struct RopePairs {
   double turns[64];
   int8_t axis[64];  // -1: behind the axes, not rotated
+  int32_t turned;   // pairs before those
 };
 
 struct RopeParams {
@@ -54,9 +55,12 @@ __device__ __forceinline__ float2 rope_cos_sin(const RopePairs* pairs, const flo
   return make_float2(c, sign * s);
 }
 
-// 8 pairs: (lo, hi) hold their first and second members (halves), or 16 neighbouring channels (interleaved).
-template <bool kInter>
-__device__ __forceinline__ void rope_unit(uint4& lo, uint4& hi, const float2* cs) {
+// 8 pairs: (lo, hi) hold their first and second members (halves), or 16 neighbouring channels (interleaved).  kPart:
+// only the first `turned` of them are rotated; the others keep their bits (a rotation by the angle 0 would not do: an
+// infinity times 0 is NaN in its partner, and a -0 becomes 0).
+template <bool kInter, bool kPart>
+__device__ __forceinline__ void rope_unit(uint4& lo, uint4& hi, const float2* cs, int turned) {
+  if (kPart && turned <= 0) return;
   float a[8], b[8];
   bf16x8_to_f32(lo, a);
   bf16x8_to_f32(hi, b);
@@ -78,11 +82,30 @@ __device__ __forceinline__ void rope_unit(uint4& lo, uint4& hi, const float2* cs
       b[i + 1] = u1 * t.w + v1 * t.z;
     }
   }
-  lo = f32_to_bf16x8(a);
-  hi = f32_to_bf16x8(b);
+  uint4 x = f32_to_bf16x8(a), y = f32_to_bf16x8(b);
+  if (kPart && turned < 8) {
+    // word w of a half holds a member each of pairs 2w and 2w + 1 (halves), or both members of a pair (interleaved)
+    const auto keep = [&](uint32_t& to, uint32_t from, int pair) {
+      const uint32_t mask = kInter ? (pair < turned ? 0u : ~0u)
+                                   : (pair < turned ? 0u : 0xffffu) | (pair + 1 < turned ? 0u : 0xffff0000u);
+      to = (to & ~mask) | (from & mask);
+    };
+    constexpr int step = kInter ? 1 : 2, second = kInter ? 4 : 0;
+    keep(x.x, lo.x, 0);
+    keep(x.y, lo.y, step);
+    keep(x.z, lo.z, 2 * step);
+    keep(x.w, lo.w, 3 * step);
+    keep(y.x, hi.x, second);
+    keep(y.y, hi.y, second + step);
+    keep(y.z, hi.z, second + 2 * step);
+    keep(y.w, hi.w, second + 3 * step);
+  }
+  lo = x;
+  hi = y;
 }
 
-template <bool kInter>
+// kPart: the axes do not cover the head (with one kernel for both, heads that they cover took 2.5 % longer).
+template <bool kInter, bool kPart>
 __global__ void __launch_bounds__(kRopeThreads) rope_axes_kernel(const __grid_constant__ RopeParams p) {
   __shared__ __align__(16) float2 cs[kRopeMaxTokens * 64];
   const int half = p.head_dim >> 1;
@@ -132,7 +155,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_axes_kernel(const __grid_co
         int tensor, gap, pair0;
         size_t at;
         locate(u, tensor, at, gap, pair0);
-        rope_unit<kInter>(lo[j], hi[j], cs + pair0);
+        rope_unit<kInter, kPart>(lo[j], hi[j], cs + pair0, p.pairs.turned - (pair0 & (half - 1)));
         uint16_t* dst = static_cast<uint16_t*>(p.out[tensor]) + at;
         *reinterpret_cast<uint4*>(dst) = lo[j];
         *reinterpret_cast<uint4*>(dst + gap) = hi[j];

@@ -84,3 +84,52 @@ def test_an_infinity_reaches_its_row(cuda_device, channel, kind, C, f32):
         name = "z" if where == "x" else "r"
         nan = np.isnan(ref[name][7])
         assert nan.all() if kind == "layer" else nan.sum() == 1
+
+
+def _bits(x):
+    return x.cpu().view(torch.int16)
+
+
+def _odd_values(x, channels):
+    """Infinities, NaN and a negative zero in some of the given channels of every third token."""
+    x = x.clone()
+    for i, v in enumerate((INF, NAN, -INF, -0.0)):
+        x[i::3, :, channels[i % len(channels)]] = v
+    return x
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("d,dims", [(64, [8, 16]), (64, [62]), (128, [6, 50]), (128, [32]), (128, [2, 2, 2])])
+def test_channels_behind_the_axes_are_copied_whatever_they_hold(cuda_device, d, dims, inter):
+    g = torch.Generator().manual_seed(3)
+    T, H, n = 50, 3, sum(dims) // 2
+    rest = list(range(2 * n, d)) if inter else list(range(n, d // 2)) + list(range(d // 2 + n, d))
+    turned = [c for c in range(d) if c not in rest]
+    pos = torch.floor(torch.rand(T, len(dims), generator=g) * 40).to(cuda_device)
+    clean = [torch.randn(T, H, d, generator=g).to(torch.bfloat16) for _ in range(2)]
+    odd = [_odd_values(x, rest[1::2] or rest) for x in clean]
+    for fn in (pa.rope_axes_fwd, pa.rope_axes_bwd):
+        want = fn(*(x.to(cuda_device) for x in clean), pos, dims, 100.0, inter)
+        got = fn(*(x.to(cuda_device) for x in odd), pos, dims, 100.0, inter)
+        for a, b, x in zip(got, want, odd):
+            assert torch.equal(_bits(a)[..., rest], x.view(torch.int16)[..., rest])
+            assert torch.equal(a[..., turned], b[..., turned])
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("d,dims", [(64, [8, 16]), (64, [62]), (128, [6, 50]), (128, [32])])
+def test_the_projection_leaves_channels_behind_the_axes(cuda_device, d, dims, inter):
+    """They are what the linear layer gives, also beside an infinity."""
+    g = torch.Generator().manual_seed(4)
+    T, C, H, n = 150, 72, 3, sum(dims) // 2
+    rest = list(range(2 * n, d)) if inter else list(range(n, d // 2)) + list(range(d // 2 + n, d))
+    x = torch.randn(T, C, generator=g).to(torch.bfloat16).to(cuda_device)
+    w = (torch.randn(3, H, d, C, generator=g) * C ** -0.5).to(torch.bfloat16)
+    w[:, 1, rest[-1], 5] = INF
+    w = w.view(3 * H * d, C).to(cuda_device)
+    pos = torch.floor(torch.rand(T, len(dims), generator=g) * 40).to(cuda_device)
+    q, k, v = pa.qkv_rope_axes_fwd(x, w, pos, H, d, dims, 100.0, inter)
+    y = pa.linear_fwd(x, w).view(T, 3, H, d)
+    assert torch.equal(_bits(v.contiguous()), _bits(y[:, 2].contiguous()))
+    for i, got in enumerate((q, k)):
+        assert torch.equal(_bits(got)[..., rest], _bits(y[:, i].contiguous())[..., rest])

@@ -319,6 +319,7 @@ int pa_block_norm_bwd(const pa_block_norm_desc* d, const void* r, const void* y,
   if (rc != PA_OK || !weights) return rc;
   pa::NormWeightParams wp;
   std::memset(&wp, 0, sizeof(wp));
+  wp.cu = p.cu;
   wp.batch = p.batch;
   wp.hidden = p.hidden;
   wp.param_f32 = p.param_f32;

@@ -869,8 +869,9 @@ __device__ __forceinline__ void slots_of(const NormSumParams& p, int32_t s, int6
   }
 }
 
-// Writes sum k of segment s at 4 channels: the raw sum where the weights' gradients need it, and the output.
-__device__ __forceinline__ void put_sum(const NormSumParams& p, int32_t s, int k, int col, float4 t) {
+// Writes sum k of segment s at 4 channels: the raw sum where the weights' gradients need it, and the output.  A segment
+// without tokens (`some` false) gets 0 whatever the weight is.
+__device__ __forceinline__ void put_sum(const NormSumParams& p, int32_t s, int k, int col, float4 t, bool some) {
   const size_t at = static_cast<size_t>(s) * p.hidden + col;
   if (k < 2 && p.sums != nullptr)
     *reinterpret_cast<float4*>(p.sums + static_cast<size_t>(k) * p.batch * p.hidden + at) = t;
@@ -878,7 +879,7 @@ __device__ __forceinline__ void put_sum(const NormSumParams& p, int32_t s, int k
   if (out == nullptr) return;
   const void* weight = k == 0 ? p.w_post : k == 1 ? p.w_pre : nullptr;
   float f[4] = {t.x, t.y, t.z, t.w};
-  if (weight != nullptr) {
+  if (weight != nullptr && some) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       f[i] *= p.param_f32 ? static_cast<const float*>(weight)[col + i]
@@ -901,7 +902,7 @@ __global__ void __launch_bounds__(kNormSumThreads) block_norm_sum_kernel(const _
   add_slots(p, c0, c1, 0, 1, col, t);
 #pragma unroll
   for (int k = 0; k < 3; ++k)
-    if (p.use >> k & 1) put_sum(p, s, k, col, t[k]);
+    if (p.use >> k & 1) put_sum(p, s, k, col, t[k], c1 > c0);
 }
 
 // Where there are few segments a block takes 128 channels of one: its 32 warps take the slots 32 apart, and the warps'
@@ -916,8 +917,7 @@ __global__ void __launch_bounds__(kNormSumLongThreads) block_norm_sum_long_kerne
   int64_t c0, c1;
   slots_of(p, s, c0, c1);
   float4 t[3];
-  if (col >= p.hidden) c1 = c0;
-  add_slots(p, c0, c1, w, 32, col, t);
+  add_slots(p, c0, col < p.hidden ? c1 : c0, w, 32, col, t);
 #pragma unroll
   for (int k = 0; k < 3; ++k) acc[k][w][lane] = t[k];
   __syncthreads();
@@ -930,10 +930,11 @@ __global__ void __launch_bounds__(kNormSumLongThreads) block_norm_sum_long_kerne
     u.z += acc[w][j][lane].z;
     u.w += acc[w][j][lane].w;
   }
-  put_sum(p, s, w, col, u);
+  put_sum(p, s, w, col, u, c1 > c0);
 }
 
 struct NormWeightParams {
+  const int32_t* cu;  // nullptr: one segment over all tokens
   int32_t batch, hidden, param_f32;
   const float* sums;  // [2][batch][C]
   const void* gate;
@@ -944,7 +945,8 @@ struct NormWeightParams {
 };
 
 // dw_post = sum_s gate[s] A[s], dw_pre = sum_s (1 + scale[s]) B[s]: one block per 32 channels and weight, its
-// 8 warps taking the segments 8 apart.
+// 8 warps taking the segments 8 apart.  The factors of a segment without tokens are not read: rows behind a padded
+// batch may hold anything, and NaN times its sum of 0 is not 0.
 __global__ void __launch_bounds__(256) block_norm_weight_kernel(const __grid_constant__ NormWeightParams p) {
   pdl_wait_primary();
   __shared__ float acc[8][32];
@@ -960,6 +962,7 @@ __global__ void __launch_bounds__(256) block_norm_weight_kernel(const __grid_con
     const float* src = p.sums + static_cast<size_t>(k) * p.batch * p.hidden + col;
 #pragma unroll 4
     for (int32_t s = w; s < p.batch; s += 8) {
+      if (p.cu != nullptr && p.cu[s + 1] <= p.cu[s]) continue;
       float m = k == 0 ? 1.f : 0.f;
       if (f != nullptr)
         m = p.param_f32

@@ -93,7 +93,8 @@ PA_API int pa_block_norm_fwd(const pa_block_norm_desc* desc, const void* x, cons
  *   r            as the forward stored it (x when y is NULL).
  *   dz           NULL exactly when pre is NONE; with dz NULL, dr and y are given.
  *   dx           may be dr (in place).       dy   NULL exactly when y is.
- *   dgate, dscale, dshift   fp32 [batch, hidden], NULL if not wanted; a segment without tokens gets 0.
+ *   dgate, dscale, dshift   fp32 [batch, hidden], NULL if not wanted; a segment without tokens gets 0 (its rows of
+ *                gate, scale and shift have no effect on anything, whatever they hold).
  *   dw_post, dw_pre         fp32 [hidden], NULL if not wanted.
  *     A gradient of something that was not given (a NULL gate, ...) must be NULL: PA_ERR_MODE.
  *   workspace    pa_block_norm_workspace_bytes(batch, total_tokens, hidden) bytes, 16-byte aligned; only read

@@ -133,3 +133,20 @@ def test_the_projection_leaves_channels_behind_the_axes(cuda_device, d, dims, in
     assert torch.equal(_bits(v.contiguous()), _bits(y[:, 2].contiguous()))
     for i, got in enumerate((q, k)):
         assert torch.equal(_bits(got)[..., rest], _bits(y[:, i].contiguous())[..., rest])
+
+
+@pytest.mark.parametrize("lens", [[0, 40, 0, 30, 0], [1] * 50 + [0] * 20])  # both ways of adding an image's sums
+def test_factors_of_images_without_tokens_have_no_effect(cuda_device, lens):
+    """Rows of the modulation behind the last image of a padded batch may hold anything."""
+    t = _inputs(lens, 264, False, 5)
+    t["w_pre"][3] = INF
+    t["w_post"][5] = -INF
+    clean, _ = _run(cuda_device, t, "rms", "layer")
+    empty = [s for s, n in enumerate(lens) if n == 0]
+    for name, v in (("gate", NAN), ("scale", INF), ("shift", NAN)):
+        t[name][empty] = v
+    got, _ = _run(cuda_device, t, "rms", "layer")
+    for name in clean:
+        assert np.array_equal(*(x[name].float().cpu().numpy() for x in (got, clean)), equal_nan=True), name
+    for name in ("dgate", "dscale", "dshift"):
+        assert not got[name][empty].any(), name

@@ -377,11 +377,11 @@ __global__ void __launch_bounds__(kNormFwdThreads, 1) block_norm_fwd_kernel(cons
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int group = w / kW, warp = w - group * kW;
   const int C = p.hidden;
-  if (threadIdx.x < fp.groups * kNormMaxStages) mbar_init(bars + threadIdx.x, 1);
-  if (threadIdx.x == 0) {
-    abort_flag = 0;
-    fence_mbar_init();
+  if (threadIdx.x < fp.groups * kNormMaxStages) {
+    mbar_init(bars + threadIdx.x, 1);
+    fence_mbar_init();  // covers this thread's own
   }
+  if (threadIdx.x == 0) abort_flag = 0;
   __syncthreads();
   if (blockIdx.x == 0 && p.cu != nullptr) check_cu(p.cu, p.batch, p.total, p.status, p.err_cu);
   const WaitCtl wc{&abort_flag, p.status, p.wait_limit_ns, p.err_timeout};
@@ -663,11 +663,11 @@ __global__ void __launch_bounds__(256, kG == 1 ? 2 : 1)
   __shared__ int abort_flag;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int C = p.hidden;
-  if (threadIdx.x < p.stages) mbar_init(bars + threadIdx.x, 1);
-  if (threadIdx.x == 0) {
-    abort_flag = 0;
-    fence_mbar_init();
+  if (threadIdx.x < p.stages) {
+    mbar_init(bars + threadIdx.x, 1);
+    fence_mbar_init();  // covers this thread's own
   }
+  if (threadIdx.x == 0) abort_flag = 0;
   __syncthreads();
   if (blockIdx.x == 0 && p.cu != nullptr) check_cu(p.cu, p.batch, p.total, p.status, p.err_cu);
   const WaitCtl wc{&abort_flag, p.status, p.wait_limit_ns, p.err_timeout};

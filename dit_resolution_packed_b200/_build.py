@@ -14,7 +14,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libpackattn.so")
 SOURCES = ["packattn.cu", "block_norm.cu", "rope_axes.cu", "sparse.cu"]
 HEADERS = ["sm100_ptx.cuh", "schedule.cuh", "attn_fwd_sm100.cuh", "attn_fwd_fp8_sm100.cuh", "attn_bwd_sm100.cuh",
-           "gemm_sm100.cuh", "exp2_poly.cuh", "host.h", "block_norm_sm100.cuh",
+           "gemm_sm100.cuh", "exp2_poly.cuh", "host.h", "row_ring.h", "block_norm_sm100.cuh",
            "rope_axes_sm100.cuh", "sparse_plan_sm100.cuh", "attn_sparse_fwd_sm100.cuh"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]

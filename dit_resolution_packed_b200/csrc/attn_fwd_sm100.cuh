@@ -208,16 +208,6 @@ __device__ __forceinline__ const void* seg_map(const FwdParams& p, int32_t seg, 
   return p.maps + (static_cast<size_t>(seg) * 3 + which) * 128;
 }
 
-// A wait used while draining after an abort: ignores the abort flag, bounded by its own limit.
-__device__ __forceinline__ bool drain_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
-  const uint32_t a = smem_u32(bar);
-  const uint64_t t0 = global_timer_ns();
-  while (!mbar_try_wait(a, parity)) {
-    if (global_timer_ns() - t0 > limit_ns) return false;
-  }
-  return true;
-}
-
 // ------------------------------------------------------------------ producer
 template <int D>
 __device__ __forceinline__ void run_producer(const FwdParams& p, uint8_t* smem, Bars* bars, const WaitCtl& wc,

@@ -17,6 +17,7 @@
 #pragma once
 #include <cstdint>
 
+#include "row_ring.h"
 #include "sm100_ptx.cuh"
 
 namespace pa {
@@ -237,14 +238,10 @@ __device__ __forceinline__ Pairs8 scale_factor(const NormParams& p, int32_t seg,
 struct RowRing {
   uint64_t* full;  // [stages]
   uint8_t* buf;
-  int stage;
-  uint32_t phase;
+  RingPlace at;
 
   __device__ __forceinline__ RowRing(uint64_t* bars, uint8_t* smem, const NormParams& p, int group)
-      : full(bars + group * kNormMaxStages),
-        buf(smem + static_cast<size_t>(group) * p.stages * p.row_bytes),
-        stage(0),
-        phase(0) {}
+      : full(bars + group * kNormMaxStages), buf(smem + static_cast<size_t>(group) * p.stages * p.row_bytes) {}
   // copies `row` of the given tensors (bytes b0 .. b3 a row; 0: not there) into stage s
   __device__ __forceinline__ void fill(const NormParams& p, int s, int64_t row, const void* t0, uint32_t b0,
                                        const void* t1, uint32_t b1, const void* t2, uint32_t b2, const void* t3,
@@ -260,21 +257,19 @@ struct RowRing {
       dst += bytes[i];
     }
   }
-  // stage and parity of the r-th row from the current one (r <= stages)
-  __device__ __forceinline__ int stage_of(const NormParams& p, int r) const {
-    return stage + r >= p.stages ? stage + r - p.stages : stage + r;
+  // the r-th row from the current one: its wait, and where it lies
+  __device__ __forceinline__ bool wait(const NormParams& p, int r, const WaitCtl& wc) const {
+    return mbar_wait(full + at.stage_of(p.stages, r), at.phase_of(p.stages, r), wc);
   }
-  __device__ __forceinline__ uint32_t phase_of(const NormParams& p, int r) const {
-    return stage + r >= p.stages ? phase ^ 1u : phase;
-  }
-  __device__ __forceinline__ const uint8_t* row(const NormParams& p, int r) const {
-    return buf + static_cast<size_t>(stage_of(p, r)) * p.row_bytes;
-  }
-  __device__ __forceinline__ void advance(const NormParams& p, int n) {
-    phase = phase_of(p, n);
-    stage = stage_of(p, n);
+  __device__ __forceinline__ uint8_t* row(const NormParams& p, int r) const {
+    return buf + static_cast<size_t>(at.stage_of(p.stages, r)) * p.row_bytes;
   }
 };
+
+// Waits, within a limit each, for the copies of the m rows from the current one on.  (Out of line: it never runs.)
+__device__ __noinline__ void drain_rows(uint64_t* full, RingPlace at, int stages, int m, uint64_t limit_ns) {
+  for (int r = 0; r < m; ++r) drain_wait(full + at.stage_of(stages, r), at.phase_of(stages, r), limit_ns);
+}
 
 // Where a group stands in its run of rows: the segment, and how far it reaches.
 struct RunCursor {
@@ -401,14 +396,13 @@ __global__ void __launch_bounds__(kNormFwdThreads, 1) block_norm_fwd_kernel(cons
   float* fa = fg + C;
   float* fb = fa + C;
   RowRing ring(bars, smem + fp.ring_offset, p, group);
-  const bool leader = warp == 0 && lane == 0;
+  bool issuing = warp == 0 && lane == 0;  // the group's copies; no longer once its wait has given up
   auto fill = [&](int s, int64_t row) {
     ring.fill(p, s, row, p.x, wide, p.y, join ? narrow : 0u, nullptr, 0u, nullptr, 0u);
   };
   int64_t row = row0 + group;  // the group's next row
-  if (leader)
-    for (int s = 0; s < p.stages && row + static_cast<int64_t>(s) * fp.groups < row1; ++s)
-      fill(s, row + static_cast<int64_t>(s) * fp.groups);
+  auto drain = [&](int m) { drain_rows(ring.full, ring.at, p.stages, m, p.wait_limit_ns); };
+  if (issuing) ring_start(p.stages, row, fp.groups, row1, fill);
 
   constexpr int kStep = kW * 256;
   // f(c, h) for the lane's channels, sweep by sweep
@@ -463,10 +457,11 @@ __global__ void __launch_bounds__(kNormFwdThreads, 1) block_norm_fwd_kernel(cons
     __syncthreads();
     span = min(at_seg.seg_end, row1);
     for (; row < span; row += fp.groups) {
-      // a copy that does not come within the limit is recorded; the row is then worked on as it lies, so that the
+      // a copy that does not come within the limit is recorded; the rows are then worked on as they lie, so that the
       // barriers still meet
-      mbar_wait(ring.full + ring.stage, ring.phase, wc);
-      uint8_t* rows = ring.buf + static_cast<size_t>(ring.stage) * p.row_bytes;
+      ring.wait(p, 0, wc);
+      const bool landed = *wc.abort_flag == 0;  // (a wait that gives up raises the flag, or has found it raised)
+      uint8_t* rows = ring.row(p, 0);
       const size_t at = static_cast<size_t>(row) * C;
       Moments m;
       float mean = 0.f, rstd = 1.f;
@@ -514,9 +509,8 @@ __global__ void __launch_bounds__(kNormFwdThreads, 1) block_norm_fwd_kernel(cons
       fence_proxy_async_smem();
       if (kW == 1) __syncwarp();
       else named_bar_sync(1 + group, kW * 32);
-      const int64_t next = row + static_cast<int64_t>(p.stages) * fp.groups;
-      if (leader && next < row1) fill(ring.stage, next);
-      ring.advance(p, 1);
+      if (issuing) issuing = ring_refill(ring.at, p.stages, row, fp.groups, 1, row1, landed, fill, drain);
+      ring.at.advance(p.stages, 1);
     }
     __syncthreads();  // the factors' readers are done
   }
@@ -682,8 +676,8 @@ __global__ void __launch_bounds__(256, kG == 1 ? 2 : 1)
   float* fa = fg + C;
   RowRing ring(bars, smem + bp.ring_offset, p, 0);
   auto fill = [&](int s, int64_t row) { ring.fill(p, s, row, p.x, br, p.dz, bz, p.dr, bd, p.y, by); };
-  if (threadIdx.x == 0)
-    for (int s = 0; s < p.stages && row0 + s < row1; ++s) fill(s, row0 + s);
+  auto drain = [&](int m) { drain_rows(ring.full, ring.at, p.stages, m, p.wait_limit_ns); };
+  if (threadIdx.x == 0) ring_start(p.stages, row0, 1, row1, fill);
 
   // first phase: group of row_warps warps
   GroupLink link;
@@ -751,9 +745,9 @@ __global__ void __launch_bounds__(256, kG == 1 ? 2 : 1)
     }
     const int n = static_cast<int>(min(static_cast<int64_t>(bp.tile), min(at_seg.seg_end, row1) - row));
 
+    if (link.group < n) ring.wait(p, link.group, wc);  // as in the forward kernel
     if (link.group < n && (front || normed)) {
       const int r = link.group;
-      mbar_wait(ring.full + ring.stage_of(p, r), ring.phase_of(p, r), wc);  // as in the forward kernel
       const uint8_t* src = ring.row(p, r);
       const BackRow<kF32> x{src, src + br, given ? src + br + bz : nullptr, src + br + bz + bd, fa, fg, C, from, step, lane};
       float4 out[2];
@@ -768,9 +762,9 @@ __global__ void __launch_bounds__(256, kG == 1 ? 2 : 1)
       }
     }
     __syncthreads();
+    // every row of the tile has been waited for; the flag is up if one has not come
+    const bool landed = *wc.abort_flag == 0;
     for (int r = team; r < n; r += bp.teams) {
-      // (with a first phase, a thread of this block has waited for each row, and the barrier above stands between)
-      if (!front && !normed) mbar_wait(ring.full + ring.stage_of(p, r), ring.phase_of(p, r), wc);
       const uint8_t* src = ring.row(p, r);
       uint8_t* dx = static_cast<uint8_t*>(p.r) + (row + r) * static_cast<int64_t>(wide);
       uint8_t* dy = static_cast<uint8_t*>(p.z) + (row + r) * static_cast<int64_t>(narrow);
@@ -818,9 +812,11 @@ __global__ void __launch_bounds__(256, kG == 1 ? 2 : 1)
       }
     }
     __syncthreads();  // the tile's stages, scalars and factors are free
-    if (threadIdx.x == 0)
-      for (int r = 0; r < n && row + r + p.stages < row1; ++r) fill(ring.stage_of(p, r), row + r + p.stages);
-    ring.advance(p, n);
+    // (that the copies have been drained is kept in the flag, not by thread, for the registers)
+    if (threadIdx.x == 0 && (landed || *wc.abort_flag != 2) &&
+        !ring_refill(ring.at, p.stages, row, 1, n, row1, landed, fill, drain))
+      *wc.abort_flag = 2;
+    ring.at.advance(p.stages, n);
     row += n;
   }
   flush(at_seg.seg);

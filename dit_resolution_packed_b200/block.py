@@ -109,6 +109,15 @@ def _check(dtype, shape, **tensors):
             raise ValueError(f"{name} must be contiguous")
 
 
+def _scratch(workspace):
+    """Address and bytes of a workspace (none, or a contiguous tensor: an expanded one has fewer bytes than elements)."""
+    if workspace is None:
+        return None, 0
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
 # ---------------------------------------------------------------- norms, gate and residual
 
 def _norm_desc(like, cu_seqlens, gate, post, w_post, residual_scale, pre, w_pre, scale, shift, eps):
@@ -195,7 +204,7 @@ def pa_block_norm_bwd(r, cu_seqlens, y, dr, dz, dx, dy, dgate, dscale, dshift, d
     _check(torch.float32, (desc.hidden,), dw_post=dw_post, dw_pre=dw_pre)
     return _library().pa_block_norm_bwd(
         ctypes.byref(desc), _p(r), _p(y), _p(dr), _p(dz), _p(dx), _p(dy), _p(dgate), _p(dscale), _p(dshift),
-        _p(dw_post), _p(dw_pre), _p(workspace), 0 if workspace is None else workspace.numel(), _handle(stream, r))
+        _p(dw_post), _p(dw_pre), *_scratch(workspace), _handle(stream, r))
 
 
 def block_norm_bwd(r, cu_seqlens=None, dr=None, dz=None, *, y=None, gate=None, post="none", w_post=None,
@@ -283,7 +292,7 @@ def pa_qkv_rope_axes_fwd(x, w_qkv, pos, dims, theta, interleaved, q, k, v, works
     _check(torch.bfloat16, (T, H, d), q=q, k=k, v=v)
     desc = _rope_desc(pos, T, dims, theta, interleaved)
     return _library().pa_qkv_rope_axes_fwd(_p(x), _p(w_qkv), _p(pos), T, C, H, d, ctypes.byref(desc), _p(q), _p(k),
-                                           _p(v), _p(workspace), workspace.numel(), _handle(stream, x))
+                                           _p(v), *_scratch(workspace), _handle(stream, x))
 
 
 def qkv_rope_axes_fwd(x, w_qkv, pos, heads, head_dim, dims, theta=10000.0, interleaved=False, stream=None):
@@ -339,8 +348,7 @@ def pa_block_select(q, k, cu_seqlens, max_seqlen, density, min_blocks, idx, cnt,
     T, H, d, B = _pack(cu_seqlens, q=q, k=k)
     width = _lists(idx, cnt, H, T // BLOCK_TOKENS + B)
     return _library().pa_block_select(_p(q), _p(k), _p(cu_seqlens), B, T, H, d, int(max_seqlen), float(density),
-                                      int(min_blocks), width, _p(idx), _p(cnt), _p(workspace), workspace.numel(),
-                                      _handle(stream, q))
+                                      int(min_blocks), width, _p(idx), _p(cnt), *_scratch(workspace), _handle(stream, q))
 
 
 def block_select(q, k, cu_seqlens, max_seqlen, density, min_blocks=1, stream=None):
@@ -378,8 +386,8 @@ def pa_block_sparse_attn_fwd(q, k, v, cu_seqlens, max_seqlen, idx, cnt, scale, o
     _check(torch.float32, (T, H), lse=lse)
     width = _lists(idx, cnt, H, T // BLOCK_TOKENS + B)
     return _library().pa_block_sparse_attn_fwd(_p(q), _p(k), _p(v), _p(cu_seqlens), B, T, H, d, int(max_seqlen),
-                                               _p(idx), _p(cnt), width, float(scale), _p(out), _p(lse), _p(workspace),
-                                               workspace.numel(), _handle(stream, q))
+                                               _p(idx), _p(cnt), width, float(scale), _p(out), _p(lse),
+                                               *_scratch(workspace), _handle(stream, q))
 
 
 def _sparse_workspace(q, cu_seqlens, max_seqlen, idx, backward):
@@ -414,7 +422,7 @@ def pa_block_sparse_attn_bwd(q, k, v, out, lse, dout, cu_seqlens, max_seqlen, id
     width = _lists(idx, cnt, H, T // BLOCK_TOKENS + B)
     return _library().pa_block_sparse_attn_bwd(_p(q), _p(k), _p(v), _p(out), _p(lse), _p(dout), _p(cu_seqlens), B, T, H,
                                                d, int(max_seqlen), _p(idx), _p(cnt), width, float(scale), _p(dq),
-                                               _p(dk), _p(dv), _p(workspace), workspace.numel(), _handle(stream, q))
+                                               _p(dk), _p(dv), *_scratch(workspace), _handle(stream, q))
 
 
 def block_sparse_attn_bwd(q, k, v, out, lse, dout, cu_seqlens, max_seqlen, idx, cnt, scale=None, stream=None):

@@ -68,6 +68,11 @@ bool sizes_ok(int32_t batch, int32_t total, int32_t heads, int32_t head_dim) {
          static_cast<int64_t>(total) * heads * head_dim < (int64_t(1) << 40);
 }
 
+// Entries of a list table (sizes_ok holds): few enough that no size formed of them passes 63 bits.
+bool table_ok(int32_t batch, int32_t total, int32_t heads, int32_t width) {
+  return block_rows(batch, total) * heads <= (int64_t(1) << 40) / std::max(width, 1);
+}
+
 int32_t keep_count(int32_t nb, double density, int32_t min_blocks) {
   return std::min(nb, std::max(min_blocks, static_cast<int32_t>(std::ceil(density * static_cast<double>(nb)))));
 }
@@ -151,7 +156,8 @@ int pa_block_select(const void* q, const void* k, const int32_t* cu_seqlens, int
                     int32_t width, int32_t* idx, int32_t* cnt, void* workspace, int64_t workspace_bytes,
                     void* stream) {
   if (head_dim != 64 && head_dim != 128) return PA_ERR_HEAD_DIM;
-  if (!sizes_ok(batch, total_tokens, heads, head_dim) || heads > 65535 || min_blocks < 1 || width < 1)
+  if (!sizes_ok(batch, total_tokens, heads, head_dim) || heads > 65535 || min_blocks < 1 || width < 1 ||
+      !table_ok(batch, total_tokens, heads, width))
     return PA_ERR_SHAPE;
   if (!(density >= 0.0 && density <= 1.0)) return PA_ERR_SCALE;
   if (batch == 0) return PA_OK;
@@ -216,7 +222,7 @@ int pa_block_select(const void* q, const void* k, const int32_t* cu_seqlens, int
 int64_t pa_block_sparse_workspace_bytes(int32_t batch, int32_t total_tokens, int32_t heads, int32_t head_dim,
                                         int32_t max_seqlen, int32_t width, int32_t backward) {
   if ((head_dim != 64 && head_dim != 128) || !sizes_ok(batch, total_tokens, heads, head_dim) || width < 0 ||
-      max_seqlen < 0)
+      max_seqlen < 0 || !table_ok(batch, total_tokens, heads, width))
     return -1;
   return layout(batch, total_tokens, heads, head_dim, max_seqlen, width, backward != 0).total;
 }
@@ -226,7 +232,8 @@ int pa_block_sparse_attn_fwd(const void* q, const void* k, const void* v, const 
                              const int32_t* idx, const int32_t* cnt, int32_t width, float scale, void* out, float* lse,
                              void* workspace, int64_t workspace_bytes, void* stream) {
   if (head_dim != 64 && head_dim != 128) return PA_ERR_HEAD_DIM;
-  if (!sizes_ok(batch, total_tokens, heads, head_dim) || width < 1) return PA_ERR_SHAPE;
+  if (!sizes_ok(batch, total_tokens, heads, head_dim) || width < 1 || !table_ok(batch, total_tokens, heads, width))
+    return PA_ERR_SHAPE;
   if (!std::isfinite(scale)) return PA_ERR_SCALE;
   if (batch == 0 || total_tokens == 0) return PA_OK;
   if (max_seqlen < 1) return PA_ERR_MAX_SEQLEN;
@@ -287,7 +294,8 @@ int pa_block_sparse_attn_bwd(const void* q, const void* k, const void* v, const 
                              const int32_t* cnt, int32_t width, float scale, void* dq, void* dk, void* dv,
                              void* workspace, int64_t workspace_bytes, void* stream) {
   if (head_dim != 64 && head_dim != 128) return PA_ERR_HEAD_DIM;
-  if (!sizes_ok(batch, total_tokens, heads, head_dim) || width < 1) return PA_ERR_SHAPE;
+  if (!sizes_ok(batch, total_tokens, heads, head_dim) || width < 1 || !table_ok(batch, total_tokens, heads, width))
+    return PA_ERR_SHAPE;
   if (!std::isfinite(scale)) return PA_ERR_SCALE;
   if (batch == 0 || total_tokens == 0) return PA_OK;
   if (max_seqlen < 1) return PA_ERR_MAX_SEQLEN;

@@ -156,8 +156,9 @@ PA_API int pa_qkv_rope_axes_fwd(const void* x, const void* w_qkv, const float* p
  *   idx   device, int32, [heads, pa_block_rows, width]: key blocks of the row's segment, increasing.
  *   cnt   device, int32, [heads, pa_block_rows]: entries of the row's list, 0 .. width.  Entries past cnt, and
  *         rows that are no block, are not read.
- * heads * head_dim is below 2^23.  Keys of a block that no list of a row names, other images' tokens and what
- * lies behind a segment's last token have no influence on the row, whatever they hold (infinities, NaN).
+ * heads * head_dim is below 2^23, and a table has at most 2^40 entries.  Keys of a block that no list of a row
+ * names, other images' tokens and what lies behind a segment's last token have no influence on the row, whatever
+ * they hold (infinities, NaN).
  */
 PA_API int64_t pa_block_rows(int32_t batch, int32_t total_tokens);
 

@@ -50,3 +50,20 @@ def test_bytes_count_whatever_the_type():
     n = pa.pa_block_sparse_workspace_bytes(1, 300, 2, 64, 300, 2, 1)
     assert list(_calls(torch.zeros(n // 8 - 1, dtype=torch.int64)))[-1]() == pa.PA_ERR_WORKSPACE
     assert list(_calls(torch.zeros(n // 8 + 1, dtype=torch.int64)))[-1]() == pa.PA_ERR_NOT_DEVICE  # host memory
+
+
+def test_a_list_table_too_wide_for_its_sizes_is_refused():
+    """Bytes of the work lists grow with rows x width: past 63 bits the product must not pass for a small size."""
+    lib = pa.load_library()
+    wide, big = 2 ** 31 - 1, 2 ** 62
+    for batch, total, heads, d in ((1 << 20, 1 << 23, 1 << 10, 64), (1, 2 ** 31 - 1, 100, 64)):
+        for backward in (0, 1):
+            assert pa.pa_block_sparse_workspace_bytes(batch, total, heads, d, total, wide, backward) == -1
+        assert lib.pa_block_sparse_attn_fwd(16, 16, 16, 16, batch, total, heads, d, total, 16, 16, wide, 0.1, 16, 16, 16,
+                                            big, None) == pa.PA_ERR_SHAPE
+        assert lib.pa_block_sparse_attn_bwd(16, 16, 16, 16, 16, 16, 16, batch, total, heads, d, total, 16, 16, wide, 0.1,
+                                            16, 16, 16, 16, big, None) == pa.PA_ERR_SHAPE
+        assert lib.pa_block_select(16, 16, 16, batch, total, heads, d, 262144, 0.5, 1, wide, 16, 16, 16, big,
+                                   None) == pa.PA_ERR_SHAPE
+    # a table of 2^40 bytes is a size like any other
+    assert pa.pa_block_sparse_workspace_bytes(1, 1 << 20, 8, 64, 1 << 20, 1 << 13, 0) > 0

@@ -150,7 +150,7 @@ def _norm_desc(like, cu_seqlens, gate, post, w_post, residual_scale, pre, w_pre,
                 raise ValueError(f"{name} needs cu_seqlens")
             if t.shape != (B, C) or t.stride(1) != 1:
                 raise ValueError(f"{name} must be [B, C] with contiguous rows")
-            strides.append(t.stride(0))
+            strides.append(t.stride(0) if B > 1 else 0)
         elif t.shape != (C,) or t.stride(0) != 1:
             raise ValueError(f"{name} must be [C], contiguous")
         at.append(t.data_ptr())

@@ -67,3 +67,12 @@ def test_a_list_table_too_wide_for_its_sizes_is_refused():
                                    None) == pa.PA_ERR_SHAPE
     # a table of 2^40 bytes is a size like any other
     assert pa.pa_block_sparse_workspace_bytes(1, 1 << 20, 8, 64, 1 << 20, 1 << 13, 0) > 0
+
+
+def test_the_stride_of_a_single_row_is_nobodys():
+    """With one image nothing steps from row to row, and the stride may be anything (1 in a tensor that came by DLPack)."""
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    cu = torch.tensor([0, 4], dtype=torch.int32)
+    row = torch.zeros(64, dtype=torch.bfloat16).as_strided((1, 64), (1, 1))
+    z = torch.empty_like(x)
+    assert pa.pa_block_norm_fwd(x, cu, None, None, z, pre="layer", scale=row, shift=row) == pa.PA_ERR_NOT_DEVICE

@@ -361,7 +361,8 @@ def block_select(q, k, cu_seqlens, max_seqlen, density, min_blocks=1, stream=Non
     T, H, d = q.shape
     B = cu_seqlens.numel() - 1
     nb = max(1, -(-int(max_seqlen) // BLOCK_TOKENS))
-    width = min(nb, max(int(min_blocks), math.ceil(density * nb)))
+    share = math.ceil(density * nb) if 0.0 <= density <= 1.0 else 0  # (else the call refuses it)
+    width = min(nb, max(int(min_blocks), share))
     with _under(stream):
         rows = T // BLOCK_TOKENS + B
         idx = q.new_empty((H, rows, max(width, 1)), dtype=torch.int32)

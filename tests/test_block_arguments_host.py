@@ -76,3 +76,11 @@ def test_the_stride_of_a_single_row_is_nobodys():
     row = torch.zeros(64, dtype=torch.bfloat16).as_strided((1, 64), (1, 1))
     z = torch.empty_like(x)
     assert pa.pa_block_norm_fwd(x, cu, None, None, z, pre="layer", scale=row, shift=row) == pa.PA_ERR_NOT_DEVICE
+
+
+@pytest.mark.parametrize("density", [float("nan"), float("inf"), -float("inf"), -0.5, 1.5])
+def test_a_density_that_is_none_is_refused_by_status(density):
+    q = torch.zeros(300, 2, 64, dtype=torch.bfloat16)
+    with pytest.raises(pa.PackAttnError) as e:
+        pa.block_select(q, q, torch.tensor([0, 300], dtype=torch.int32), 300, density)
+    assert e.value.code == pa.PA_ERR_SCALE

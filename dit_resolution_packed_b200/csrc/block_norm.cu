@@ -308,12 +308,15 @@ int pa_block_norm_bwd(const pa_block_norm_desc* d, const void* r, const void* y,
   sp.use = (dgate || dw_post ? 1 : 0) | (dscale || dw_pre ? 2 : 0) | (dshift ? 4 : 0);
   // Some 40 segments fill the GPU; with fewer, a segment's slots are read in parallel.  The whole backward of
   // 65536 x 1152 by one and the other: 3 segments 224 and 195 us, 16 201 and 194, 32 197.5 and 196, 48 197.5 and 200,
-  // 256 196 and 229, 2048 220 and 488.
-  if (p.batch > 40)
-    rc = pa::host::launch_behind(pa::block_norm_sum_kernel,
-                                 dim3(p.batch, (p.hidden + 4 * pa::kNormSumThreads - 1) / (4 * pa::kNormSumThreads)),
-                                 pa::kNormSumThreads, 0, call.stream, sp);
-  else
+  // 256 196 and 229, 2048 220 and 488.  (A long one among many has blocks of its own: the kernel.)
+  if (p.batch > 40) {
+    const int32_t by = div_up(p.hidden, 4 * pa::kNormSumThreads);
+    sp.long_runs = std::max(1, 32 / s.teams);  // 32 slots, one for each part of a long segment
+    sp.long_col_blocks = div_up(p.hidden, 32 * by);
+    const int64_t blocks = p.batch + static_cast<int64_t>(div_up(p.chunks, sp.long_runs)) * sp.long_col_blocks;
+    rc = pa::host::launch_behind(pa::block_norm_sum_kernel, dim3(static_cast<unsigned>(blocks), by), pa::kNormSumThreads,
+                                 0, call.stream, sp);
+  } else
     rc = pa::host::launch_behind(pa::block_norm_sum_long_kernel, dim3(p.batch, (p.hidden + 127) / 128),
                                  pa::kNormSumLongThreads, 0, call.stream, sp);
   if (rc != PA_OK || !weights) return rc;

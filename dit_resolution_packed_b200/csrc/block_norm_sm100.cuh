@@ -826,6 +826,8 @@ struct NormSumParams {
   const int32_t* cu;  // nullptr: one segment over all tokens
   int32_t total, batch, hidden, rows_per_chunk, chunks, teams, param_f32;
   int32_t use;  // bit k: sum k (A, B, S) is needed
+  int32_t long_runs;         // block_norm_sum_kernel: a segment of more runs of rows is a long one
+  int32_t long_col_blocks;   // ... and takes this many blocks of each of the grid's rows
   const float* part;
   float* sums;  // [2][batch][C]: A and B of every segment, nullptr: not needed
   const void* w_post;
@@ -884,21 +886,51 @@ __device__ __forceinline__ void put_sum(const NormSumParams& p, int32_t s, int k
   *reinterpret_cast<float4*>(out + at) = make_float4(f[0], f[1], f[2], f[3]);
 }
 
-// Per segment: the sum of its slots, in order.  Where there are many segments a thread takes 4 channels of one, slot
-// after slot (a short image has one or two).
+// Per segment: the sum of its slots.  Where there are many segments a thread takes 4 channels of one, slot after slot (a
+// short image has one or two).  A long one among them would keep a few threads busy for the whole call (602 us for one
+// of 65536 tokens and 40 of 200, 256 channels; 168 us as it is), so its channels go 32 a block to blocks of
+// their own behind those of the segments, the slots 32 apart and the 32 parts added in order.  A segment of more than
+// long_runs runs holds the first row of a run whose number is a multiple of long_runs; the first such row names it, and
+// block j of these looks for its segment there.
 constexpr int kNormSumThreads = 256;
 __global__ void __launch_bounds__(kNormSumThreads) block_norm_sum_kernel(const __grid_constant__ NormSumParams p) {
   pdl_wait_primary();
-  const int col = (blockIdx.y * kNormSumThreads + threadIdx.x) * 4;
-  if (col >= p.hidden) return;
-  const int32_t s = blockIdx.x;
+  __shared__ float4 acc[3][32][8];
   int64_t c0, c1;
-  slots_of(p, s, c0, c1);
   float4 t[3];
-  add_slots(p, c0, c1, 0, 1, col, t);
+  const int64_t most = static_cast<int64_t>(p.long_runs) * p.teams;  // slots
+  if (blockIdx.x < p.batch) {
+    const int col = (blockIdx.y * kNormSumThreads + threadIdx.x) * 4;
+    const int32_t s = blockIdx.x;
+    slots_of(p, s, c0, c1);
+    if (col >= p.hidden || c1 - c0 > most) return;
+    add_slots(p, c0, c1, 0, 1, col, t);
 #pragma unroll
-  for (int k = 0; k < 3; ++k)
-    if (p.use >> k & 1) put_sum(p, s, k, col, t[k], c1 > c0);
+    for (int k = 0; k < 3; ++k)
+      if (p.use >> k & 1) put_sum(p, s, k, col, t[k], c1 > c0);
+    return;
+  }
+  const int32_t j = (blockIdx.x - p.batch) / p.long_col_blocks, rest = (blockIdx.x - p.batch) - j * p.long_col_blocks;
+  const int64_t stride = static_cast<int64_t>(p.long_runs) * p.rows_per_chunk, row = j * stride;
+  const int32_t s = segment_of(p.cu, p.batch, static_cast<int32_t>(row), threadIdx.x & 31);
+  slots_of(p, s, c0, c1);
+  if (c1 - c0 <= most || (p.cu[s] + stride - 1) / stride != j) return;
+  const int lane = threadIdx.x & 7, part = threadIdx.x >> 3;
+  const int col = (rest * gridDim.y + blockIdx.y) * 32 + lane * 4;
+  add_slots(p, c0, col < p.hidden ? c1 : c0, part, 32, col, t);
+#pragma unroll
+  for (int k = 0; k < 3; ++k) acc[k][part][lane] = t[k];
+  __syncthreads();
+  if (part >= 3 || col >= p.hidden || !(p.use >> part & 1)) return;
+  float4 u = acc[part][0][lane];
+#pragma unroll 8
+  for (int i = 1; i < 32; ++i) {
+    u.x += acc[part][i][lane].x;
+    u.y += acc[part][i][lane].y;
+    u.z += acc[part][i][lane].z;
+    u.w += acc[part][i][lane].w;
+  }
+  put_sum(p, s, part, col, u, true);
 }
 
 // Where there are few segments a block takes 128 channels of one: its 32 warps take the slots 32 apart, and the warps'

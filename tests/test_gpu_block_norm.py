@@ -292,3 +292,11 @@ def test_bad_cu_seqlens_is_recorded(cuda_device):
         assert pa.pa_get_error() == pa.PA_ERR_CU_SEQLENS
         pa.block_norm_bwd(d["x"], cu, d["dr"], d["dz"], y=d["y"], gate=d["gate"], pre="layer")
         assert pa.pa_get_error() == pa.PA_ERR_CU_SEQLENS
+
+
+@pytest.mark.parametrize("C", [72, 264, 520, 1152, 2056])
+@pytest.mark.parametrize("lens", [[2500] + [3] * 45, [3] * 30 + [0, 1500] + [1] * 12 + [0, 1200, 0],
+                                  [10, 75] * 30, [180] * 41])
+def test_long_images_among_many(cuda_device, lens, C):
+    """More images than the sums take one by one, some of them over many runs of rows."""
+    _run(cuda_device, _case(lens, C, False, 16), "rms", "layer")

@@ -24,7 +24,7 @@ namespace pa {
 
 constexpr int kNormMaxHidden = 8192;
 constexpr int kNormMaxStages = 8;   // rows in flight per group
-constexpr int kNormMaxTile = 12;       // rows of a tile (backward)
+constexpr int kNormMaxTile = 8;        // rows of a tile (backward): a block has 8 warps at most
 constexpr int kNormMaxBwdStages = 24;  // rows in flight per block (backward)
 constexpr int kNormFwdThreads = 768;  // most threads of a block (forward)
 

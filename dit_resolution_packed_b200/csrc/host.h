@@ -39,8 +39,6 @@ class Call {
 
 // Tensor map of a bf16 [rows, heads * head_dim] matrix, box 64 columns x 128 rows, 128-byte swizzle.
 bool encode_rows(CUtensorMap* m, const void* base, int32_t rows, int32_t heads, int32_t head_dim);
-// Tensor map of a bf16 row-major [outer, inner] matrix, box {64, box_outer}, 128-byte swizzle.
-bool encode_matrix(CUtensorMap* m, const void* base, int64_t inner, int64_t outer, uint32_t box_outer);
 
 // Positions with several axes (rope_axes.cu): PA_OK or why a description is refused; the pairs of a head that belong
 // to an axis; the (cos, sin) of every token and pair into `table`.

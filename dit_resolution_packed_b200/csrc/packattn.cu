@@ -411,9 +411,6 @@ Call::~Call() {
 bool encode_rows(CUtensorMap* m, const void* base, int32_t rows, int32_t heads, int32_t head_dim) {
   return encode_map(m, base, rows, heads, head_dim);
 }
-bool encode_matrix(CUtensorMap* m, const void* base, int64_t inner, int64_t outer, uint32_t box_outer) {
-  return encode_2d(m, base, inner, outer, box_outer);
-}
 
 }  // namespace host
 }  // namespace pa

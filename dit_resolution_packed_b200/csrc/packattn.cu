@@ -324,20 +324,8 @@ int launch_gemm(const pa::GemmParams& gp, int dev, cudaStream_t stream, bool ove
   const int64_t tiles = ((static_cast<int64_t>(gp.M) + pa::kGemmBM - 1) / pa::kGemmBM) *
                         ((static_cast<int64_t>(gp.N) + pa::kGemmBN - 1) / pa::kGemmBN);
   const int grid = static_cast<int>(std::min<int64_t>(g_dev[dev].sms, tiles));
-  if (overlap) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(pa::kGemmThreads);
-    cfg.dynamicSmemBytes = pa::kGemmSmemBytes;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, pa::gemm_kernel<kEpi>, gp) != cudaSuccess) return PA_ERR_CUDA;
-    return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
-  }
+  if (overlap)
+    return pa::host::launch_behind(pa::gemm_kernel<kEpi>, grid, pa::kGemmThreads, pa::kGemmSmemBytes, stream, gp);
   pa::gemm_kernel<kEpi><<<grid, pa::kGemmThreads, pa::kGemmSmemBytes, stream>>>(gp);
   return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

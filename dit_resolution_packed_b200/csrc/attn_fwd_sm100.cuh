@@ -802,20 +802,4 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
   }
 }
 
-// A one-warp kernel that waits on a barrier nothing completes, through the same
-// bounded wait as the attention kernel; it must record a timeout and return.
-static __global__ void wait_timeout_selftest_kernel(int32_t* status, uint64_t limit_ns, int32_t err_timeout) {
-  __shared__ uint64_t bar;
-  __shared__ int abort_flag;
-  if (threadIdx.x == 0) {
-    mbar_init(&bar, 1);
-    abort_flag = 0;
-    fence_mbar_init();
-  }
-  __syncthreads();
-  const WaitCtl wc{&abort_flag, status, limit_ns, err_timeout};
-  mbar_wait(&bar, 0, wc);
-  __syncthreads();
-}
-
 }  // namespace pa

@@ -232,6 +232,22 @@ int64_t fp8_vt_keys(int32_t batch, int32_t total) {
   return 16 * ((static_cast<int64_t>(total) + 15) / 16) + 16 * static_cast<int64_t>(batch);
 }
 
+// A one-warp kernel that waits on a barrier nothing completes, through the same
+// bounded wait as the attention kernels; it must record a timeout and return.
+__global__ void wait_timeout_selftest_kernel(int32_t* status, uint64_t limit_ns, int32_t err_timeout) {
+  __shared__ uint64_t bar;
+  __shared__ int abort_flag;
+  if (threadIdx.x == 0) {
+    pa::mbar_init(&bar, 1);
+    abort_flag = 0;
+    pa::fence_mbar_init();
+  }
+  __syncthreads();
+  const pa::WaitCtl wc{&abort_flag, status, limit_ns, err_timeout};
+  pa::mbar_wait(&bar, 0, wc);
+  __syncthreads();
+}
+
 // Events around the main kernel of a call when profiling is on (ev0 recorded here).
 int prof_begin(cudaStream_t stream, cudaEvent_t* ev1) {
   *ev1 = nullptr;
@@ -883,8 +899,8 @@ int pa_selftest_wait_timeout(uint32_t limit_us, void* stream_handle) {
   if (cudaSetDevice(dev) != cudaSuccess) return PA_ERR_CUDA;
   StreamState* st = state_for(dev, stream);
   if (ensure_status(st) != PA_OK) return PA_ERR_CUDA;
-  pa::wait_timeout_selftest_kernel<<<1, 32, 0, stream>>>(st->status, static_cast<uint64_t>(limit_us) * 1000ull,
-                                                         PA_ERR_TIMEOUT);
+  wait_timeout_selftest_kernel<<<1, 32, 0, stream>>>(st->status, static_cast<uint64_t>(limit_us) * 1000ull,
+                                                     PA_ERR_TIMEOUT);
   return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 

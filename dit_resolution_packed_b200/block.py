@@ -3,7 +3,8 @@
 As in the package's other bindings, the functions named ``pa_*`` mirror the C ABI and only marshal arguments;
 the others allocate outputs and scratch memory, call them and raise on a host-side error status.  Outputs and
 scratch come from torch's allocator under ``stream`` (default: the current stream of the tensors' device), so
-they may be freed or captured into a graph like any other tensor of that stream.
+they may be freed or captured into a graph like any other tensor of that stream.  None of them is known to autograd: a
+forward call does not record its backward, which is the ``_bwd`` beside it.
 """
 import contextlib
 import ctypes

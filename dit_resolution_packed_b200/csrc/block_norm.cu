@@ -49,8 +49,9 @@ void split_bwd_rows(BwdSplit* s, int32_t hidden, int32_t row_bytes) {
   s->stages = std::min(pa::kNormMaxBwdStages,
                        std::max(1, (kSmemPerSm / s->per_sm - s->ring_offset) / std::max(1, row_bytes)));
   // as few warps a row as keep three quarters of the block's warps at work on a tile's rows, and never more than the
-  // block has: a group's barrier counts all its warps.  Measured by this rule, with one and with all warps a row, us:
-  // 16384 x 2048 110, 112, 110; 8192 x 4096 111, 122, 110; 4096 x 8192 132, 169, 132; 1152 and 1536 channels alike.
+  // block has: a group's barrier counts all its warps.  Measured by this rule, with one and with as many warps a row as
+  // the block has, us: 16384 x 1152 73, 73, 137; 16384 x 2048 110, 112, 210; 8192 x 4096 108, 118, 157; 4096 x 8192
+  // 129, 168, 143.
   s->row_warps = 1;
   while (2 * s->row_warps <= warps && 4 * s->row_warps * std::min(warps / s->row_warps, s->stages) < 3 * warps)
     s->row_warps *= 2;
@@ -115,12 +116,12 @@ int64_t sum_floats(int32_t batch, int32_t hidden) { return 2 * static_cast<int64
 // The forward's blocks: one per SM, groups of `warps` warps, each with a ring of rows behind the factors.
 // Warps a row: what a row costs whatever its width (shuffles, barriers) is paid by each of its warps, against which
 // long rows leave too few in shared memory for one warp each.  Measured with 1, 2 and 4 warps, bf16 / fp32 residual, us:
-//     16384 x 1536   42.3 / 58.5   45.2 / 57.9    63.6 / 73.2
-//     16384 x 2304   60.7 / 83.2   62.9 / 82.2    74.7 / 89.7
-//     16384 x 2560   68.2 / 93.7   66.9 / 90.1    76.4 / 97.5
-//      8192 x 3584   57.0 / 85.2   52.7 / 77.3    55.8 / 74.4
-//      8192 x 4096   70.1 / 93.0   63.5 / 85.5    59.6 / 81.1
-//      4096 x 8192    138 / 237     106 / 174     84.1 / 118
+//     16384 x 1536   42.8 / 57.5   45.6 / 58.0    65.5 / 74.8
+//     16384 x 2304   61.7 / 84.1   63.3 / 83.5    78.2 / 91.8
+//     16384 x 2560   68.6 / 94.2   67.6 / 91.1    79.2 / 99.5
+//      8192 x 3584   57.8 / 85.8   53.2 / 78.2    56.9 / 75.8
+//      8192 x 4096   71.4 / 93.0   64.5 / 85.6    60.6 / 81.9
+//      4096 x 8192    140 / 237     106 / 175     84.4 / 120
 struct FwdSplit {
   int32_t warps, groups, rows, blocks, stages, row_bytes, ring_offset;
   int threads() const { return warps * groups * 32; }
@@ -134,8 +135,10 @@ FwdSplit split_fwd(int32_t total, int32_t hidden, int32_t row_bytes) {
   const int room = (kSmemPerSm - s.ring_offset) / row_bytes;  // rows
   const int most = pa::kNormFwdThreads / 32 / s.warps;
   s.rows = div_up(total, kSms);
-  // rows for two groups of three to be worked on and for one on its way (with half as many groups the same time,
-  // with a group for every row no better); more where there is room, and no more groups than rows
+  // groups for two thirds of the rows that fit (with half as many the same time, with one for every row no better), no
+  // more than rows, and whole stages of what fits for each: more than one only where `most` or the rows limit the groups
+  // (joined rows below about 1050 bf16 or 710 fp32 channels, or a short pack).  With one stage a group asks for its next
+  // row when it is done with the current one, and what overlaps the copy is the other groups' work.
   s.groups = std::max(1, std::min({most, room * 2 / 3, s.rows}));
   s.stages = std::max(1, std::min(pa::kNormMaxStages, room / s.groups));
   s.blocks = div_up(total, s.rows);
@@ -306,9 +309,9 @@ int pa_block_norm_bwd(const pa_block_norm_desc* d, const void* r, const void* y,
   sp.dscale = dscale;
   sp.dshift = dshift;
   sp.use = (dgate || dw_post ? 1 : 0) | (dscale || dw_pre ? 2 : 0) | (dshift ? 4 : 0);
-  // Some 40 segments fill the GPU; with fewer, a segment's slots are read in parallel.  The whole backward of
-  // 65536 x 1152 by one and the other: 3 segments 224 and 195 us, 16 201 and 194, 32 197.5 and 196, 48 197.5 and 200,
-  // 256 196 and 229, 2048 220 and 488.  (A long one among many has blocks of its own: the kernel.)
+  // Some 40 segments fill the GPU; with fewer, every segment's slots are read in parallel.  The whole backward of
+  // 65536 x 1152 by one and the other: 3 segments 195 and 196 us, 16 204 and 195, 24 202 and 198, 32 200 and 198, 48 199
+  // and 200, 256 198 and 231, 2048 223 and 492.  (A long one among many has blocks of its own: the kernel.)
   if (p.batch > 40) {
     const int32_t by = div_up(p.hidden, 4 * pa::kNormSumThreads);
     sp.long_runs = std::max(1, 32 / s.teams);  // 32 slots, one for each part of a long segment

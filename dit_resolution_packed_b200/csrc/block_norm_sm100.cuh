@@ -1,9 +1,9 @@
 // block_norm_sm100.cuh -- the join between two blocks of a packed stream, and its gradients:
 //     u = N_post(y) w_post,   r = residual_scale x + gate[s] u,   z = N_pre(r) w_pre (1 + scale[s]) + shift[s].
 //
-// The bound is memory: every tensor is read once and written once.  A block takes a run of neighbouring rows (tokens)
-// and bulk copies bring its next rows into shared memory while it works on the current ones, so the bytes in flight
-// do not depend on registers.
+// The bound is memory: every tensor is read once and written once.  A block takes a run of neighbouring rows (tokens),
+// which bulk copies bring into shared memory, so the bytes in flight do not depend on registers: as many rows as fit, some
+// of them worked on and the others on their way.
 //
 // Statistics: a warp sums its channels and their squares around a pivot of its own (the mean of its first sweep of
 // 256), which gives its (mean, M2); where several warps share a row, theirs are merged the same way around the first

@@ -7,9 +7,11 @@
 // size has to be read back from the device.  Pairs of blocks (256) and groups of eight (1024) are numbered alike.
 //
 // Selection.  The score of (query block, key block) is the inner product of their mean vectors.  Means, products
-// and sums are fp64: a sum of 128 bf16 values is exact there, so the order of two scores does not depend on the
-// order of the additions, and a selection can be reproduced.  It reads q and k once (memory-bound); the scores
-// themselves are d products per pair of blocks, 1/16384 of the attention's.
+// and sums are fp64.  A sum of 128 bf16 values is exact there while their exponents lie within 38 of each other; the
+// division by the tokens of a short block and the products' sum round, in an order that is fixed (so a selection repeats
+// itself, and equal means give equal scores).  Scores that differ by a few roundings of 64 bits may be ordered either
+// way by another order of additions.  It reads q and k once (memory-bound); the scores themselves are d products per
+// pair of blocks, 1/16384 of the attention's.
 #pragma once
 #include <cuda.h>
 

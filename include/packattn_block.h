@@ -166,7 +166,8 @@ PA_API int64_t pa_block_rows(int32_t batch, int32_t total_tokens);
  * pa_block_select -- write idx and cnt: for each head and query block of a segment of nb blocks, the
  *     min(nb, max(min_blocks, ceil(density * nb)))
  * key blocks whose mean key has the largest inner product with the block's mean query, in increasing order
- * (means and products in fp64; equal scores: the lower block first; a NaN score ranks last, as -infinity).
+ * (means and products in fp64, in a fixed order of additions; scores that come out equal: the lower block first; a
+ * NaN score ranks last, as -infinity).
  * Unused entries are -1, rows that are no block have cnt 0.
  *   q, k          as for pa_varlen_attn_fwd.     max_seqlen  an upper bound of every segment, <= 262144.
  *   density       0 .. 1 (fp64).                 min_blocks  >= 1.

@@ -494,7 +494,9 @@ int pa_varlen_attn_fwd(const void* q, const void* k, const void* v, const int32_
                                      static_cast<uint64_t>(heads) * head_dim * 2, true);
   const void* bases[3] = {q, k, v};
   for (int i = 0; i < 3; ++i) {
-    if (!encode_map(&sp.tmpl[i], bases[i], total_tokens, heads, head_dim)) return PA_ERR_CUDA;
+    if (!encode_map(&sp.tmpl[i], bases[i], total_tokens, heads, head_dim) ||
+        !encode_map(&sp.small[i], bases[i], 1, heads, head_dim))
+      return PA_ERR_CUDA;
     sp.base[i] = bases[i];
   }
   pa::schedule_kernel<<<1, pa::kSchedThreads, 0, stream>>>(sp);
@@ -973,7 +975,9 @@ int pa_varlen_attn_fwd_noalloc(const void* q, const void* k, const void* v, cons
                                      static_cast<uint64_t>(heads) * head_dim * 2, true);
   const void* bases[3] = {q, k, v};
   for (int i = 0; i < 3; ++i) {
-    if (!encode_map(&sp.tmpl[i], bases[i], total_tokens, heads, head_dim)) return PA_ERR_CUDA;
+    if (!encode_map(&sp.tmpl[i], bases[i], total_tokens, heads, head_dim) ||
+        !encode_map(&sp.small[i], bases[i], 1, heads, head_dim))
+      return PA_ERR_CUDA;
     sp.base[i] = bases[i];
   }
   pa::schedule_kernel<<<1, pa::kSchedThreads, 0, stream>>>(sp);
@@ -1128,12 +1132,14 @@ int pa_varlen_attn_fwd_fp8(const void* q8, const void* k8, const void* v8t, cons
   pa::SchedParams sp = forward_sched(cu_seqlens, st->status, st->ws, L, batch, total_tokens, heads, max_seqlen,
                                      static_cast<uint64_t>(hd), false);
   if (!encode_u8(&sp.tmpl[0], q8, hd, total_tokens, hd) || !encode_u8(&sp.tmpl[1], k8, hd, total_tokens, hd) ||
-      !encode_u8(&sp.tmpl[2], v8t, vt_keys, hd, vt_keys))
+      !encode_u8(&sp.tmpl[2], v8t, vt_keys, hd, vt_keys) || !encode_u8(&sp.small[0], q8, hd, 1, hd) ||
+      !encode_u8(&sp.small[1], k8, hd, 1, hd) || !encode_u8(&sp.small[2], v8t, 1, hd, vt_keys))
     return PA_ERR_CUDA;
   sp.base[0] = q8;
   sp.base[1] = k8;
   sp.base[2] = v8t;
   sp.v_keys_inner = 1;
+  sp.v_rows_bytes = static_cast<uint64_t>(hd - 1) * vt_keys;
   pa::schedule_kernel<<<1, pa::kSchedThreads, 0, stream>>>(sp);
   if (cudaGetLastError() != cudaSuccess) return PA_ERR_CUDA;
 

@@ -69,6 +69,7 @@ __host__ __device__ constexpr int32_t group_len(int32_t info) { return (info >> 
 
 struct SchedParams {
   CUtensorMap tmpl[3];     // q, k, v over the whole [T, H*d] matrix (host-encoded)
+  CUtensorMap small[3];    // the same, encoded as a tensor of a row (write_part_map)
   const void* base[3];     // q, k, v base pointers
   const int32_t* cu;       // [B+1]
   int32_t* status;         // status word
@@ -85,6 +86,7 @@ struct SchedParams {
   // starts at key 16*ceil(cu[s]/16) + 16*s (the FP8 variant's transposed V); its
   // per-segment map moves the base to that key and sets the key extent to L
   int32_t v_keys_inner;
+  uint64_t v_rows_bytes;   // then: bytes from the first channel's row to the last one's
   int32_t err_cu, err_max;  // status codes to record
   int32_t group_short;      // nonzero (and info set): pack consecutive short segments into shared tiles
 };
@@ -289,18 +291,15 @@ __global__ void __launch_bounds__(kSchedThreads, 1) schedule_kernel(const __grid
     const int32_t span = unit_span(len, unit_of(s));
     if (span <= 0) continue;
     uint8_t* dst = p.maps + static_cast<size_t>(idx) * 128;
-    const uint4* src = reinterpret_cast<const uint4*>(&p.tmpl[which]);
-#pragma unroll
-    for (int w = 0; w < 8; ++w) reinterpret_cast<uint4*>(dst)[w] = src[w];
     if (which == 2 && p.v_keys_inner) {
       const uint64_t key0 = 16ull * ((static_cast<uint64_t>(beg) + 15) / 16) + 16ull * static_cast<uint64_t>(s);
-      tmap_replace_address(dst, static_cast<const uint8_t*>(p.base[2]) + key0);
-      tmap_replace_dim0(dst, static_cast<uint32_t>(span));
+      write_part_map<0>(dst, p.tmpl[2], p.small[2], p.v_rows_bytes + span, static_cast<const uint8_t*>(p.base[2]) + key0,
+                        static_cast<uint32_t>(span));
       continue;
     }
     const uint8_t* seg_base = static_cast<const uint8_t*>(p.base[which]) + static_cast<uint64_t>(beg) * p.row_bytes;
-    tmap_replace_address(dst, seg_base);
-    tmap_replace_dim1(dst, static_cast<uint32_t>(span));
+    write_part_map<1>(dst, p.tmpl[which], p.small[which], static_cast<uint64_t>(span) * p.row_bytes, seg_base,
+                      static_cast<uint32_t>(span));
   }
 
   // 5. bucket offsets in descending key order (each thread owns 4 buckets)

@@ -253,7 +253,9 @@ int pa_block_sparse_attn_fwd(const void* q, const void* k, const void* v, const 
                                        width, false, call.status);
   const void* bases[3] = {q, k, v};
   for (int i = 0; i < 3; ++i) {
-    if (!pa::host::encode_rows(&p.tmpl[i], bases[i], total_tokens, heads, head_dim)) return PA_ERR_CUDA;
+    if (!pa::host::encode_rows(&p.tmpl[i], bases[i], total_tokens, heads, head_dim) ||
+        !pa::host::encode_rows(&p.small[i], bases[i], 1, heads, head_dim))
+      return PA_ERR_CUDA;
     p.base[i] = bases[i];
   }
   const int64_t items = p.units * heads;
@@ -318,7 +320,9 @@ int pa_block_sparse_attn_bwd(const void* q, const void* k, const void* v, const 
                                        width, true, call.status);
   const void* bases[4] = {q, k, v, dout};
   for (int i = 0; i < 4; ++i) {
-    if (!pa::host::encode_rows(&p.tmpl[i], bases[i], total_tokens, heads, head_dim)) return PA_ERR_CUDA;
+    if (!pa::host::encode_rows(&p.tmpl[i], bases[i], total_tokens, heads, head_dim) ||
+        !pa::host::encode_rows(&p.small[i], bases[i], 1, heads, head_dim))
+      return PA_ERR_CUDA;
     p.base[i] = bases[i];
   }
   const int64_t items = p.units * heads;

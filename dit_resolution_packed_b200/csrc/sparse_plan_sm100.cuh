@@ -262,6 +262,7 @@ __global__ void __launch_bounds__(256) select_topk_kernel(const __grid_constant_
 // ---------------------------------------------------------------- work lists
 struct SparsePlanParams {
   CUtensorMap tmpl[4];     // q, k, v[, dout] over the whole [T, H*d] matrix
+  CUtensorMap small[4];    // the same, encoded as a tensor of a row (write_part_map)
   const void* base[4];
   const int32_t* cu;
   const int32_t* idx;      // [H][rows][width]
@@ -292,11 +293,9 @@ __device__ __forceinline__ void write_maps(const SparsePlanParams& p, int64_t se
   const int32_t beg = __ldg(p.cu + seg), end = __ldg(p.cu + seg + 1);
   if (beg < 0 || end <= beg || end > p.total) return;  // no units
   uint8_t* dst = p.maps + (static_cast<size_t>(seg) * p.n_maps + lane) * 128;
-  const uint4* src = reinterpret_cast<const uint4*>(&p.tmpl[lane]);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) reinterpret_cast<uint4*>(dst)[i] = src[i];
-  tmap_replace_address(dst, static_cast<const uint8_t*>(p.base[lane]) + static_cast<uint64_t>(beg) * p.row_bytes);
-  tmap_replace_dim1(dst, static_cast<uint32_t>(end - beg));
+  write_part_map<1>(dst, p.tmpl[lane], p.small[lane], static_cast<uint64_t>(end - beg) * p.row_bytes,
+                    static_cast<const uint8_t*>(p.base[lane]) + static_cast<uint64_t>(beg) * p.row_bytes,
+                    static_cast<uint32_t>(end - beg));
   fence_tmap_release();
 }
 

@@ -8,6 +8,7 @@ import pytest
 import torch
 
 import dit_resolution_packed_b200 as pa
+import workloads
 from oracle import block as ob
 
 pytestmark = pytest.mark.gpu
@@ -150,3 +151,45 @@ def test_factors_of_images_without_tokens_have_no_effect(cuda_device, lens):
         assert np.array_equal(*(x[name].float().cpu().numpy() for x in (got, clean)), equal_nan=True), name
     for name in ("dgate", "dscale", "dshift"):
         assert not got[name][empty].any(), name
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("value", [NAN, INF, -INF])
+@pytest.mark.parametrize("where", ["q", "k", "v", "dout"])
+def test_attention_over_a_listed_key_that_is_not_finite(cuda_device, where, value, d):
+    """NaN where the formulas give it, whichever key of a tile it is (some exponentials are polynomials), in the first tile
+    of a row and in later ones; the dense calls too."""
+    lens, H, row_blocks = [300, 40], 2, 3
+    p = workloads.random_pack(lens, H, d, 41)
+    clean = {n: p[n] for n in ("q", "k", "v")}
+    clean["dout"] = workloads.random_dout(p["q"].shape, 42)
+    cu, rows = p["cu_seqlens"], ob.table_rows(2, 340)
+    cnt = torch.zeros(H, rows, dtype=torch.int32)
+    idx = torch.arange(row_blocks, dtype=torch.int32).repeat(H, rows, 1)
+    for s, n in enumerate(lens):
+        first = ob.first_row(cu.numpy(), s)
+        cnt[:, first:first + ob.n_blocks(n)] = ob.n_blocks(n)
+    gc, gi, gn = cu.to(cuda_device), idx.to(cuda_device), cnt.to(cuda_device)
+    scale = d ** -0.5
+    g = {n: x.to(cuda_device) for n, x in clean.items()}
+    out, lse = pa.block_sparse_attn_fwd(g["q"], g["k"], g["v"], gc, 300, gi, gn)
+    for at in list(range(8)) + [133, 262]:
+        t = dict(clean, **{where: clean[where].clone()})
+        t[where][at, 0, 5] = value
+        g = {n: x.to(cuda_device) for n, x in t.items()}
+        runs = [(pa.block_sparse_attn_fwd(g["q"], g["k"], g["v"], gc, 300, gi, gn),
+                 pa.block_sparse_attn_bwd(g["q"], g["k"], g["v"], out, lse, g["dout"], gc, 300, gi, gn)),
+                (pa.varlen_attn_fwd(g["q"], g["k"], g["v"], gc, 300),
+                 pa.varlen_attn_bwd(g["q"], g["k"], g["v"], out, lse, g["dout"], gc, 300))]
+        assert pa.pa_get_error() == pa.PA_OK
+        # the oracle of the first image alone, whose every pair is visible: over the whole pack its matrix products would
+        # take 0 times NaN for the pairs of different images
+        one = [t[n][:300] for n in ("q", "k", "v")]
+        lists = np.array([0, 300]), idx[:, :3].numpy(), cnt[:, :3].numpy(), scale
+        with np.errstate(all="ignore"):
+            want = ob.sparse_attention(*one, *lists)
+            want += ob.sparse_attention_bwd(*one, out[:300], lse[:300], t["dout"][:300], *lists)
+        for form, got in zip(("sparse", "dense"), runs):
+            for name, a, b in zip(("out", "lse", "dq", "dk", "dv"), got[0] + got[1], want):
+                nan = torch.isnan(a.float()).cpu().numpy()
+                assert np.array_equal(nan[:300], np.isnan(b)) and not nan[300:].any(), f"{form} {name}, token {at}"

@@ -500,7 +500,7 @@ __device__ __forceinline__ void run_mma(const FwdParams& p, uint8_t* smem, Bars*
 // Row extreme of the 128 scores (64 register pairs): max (kNeg = false) or min
 // (kNeg = true, for a negative scale), only keys in [kv_lo, kv_hi) when kPartial.
 // Eight independent chains of three-input max/min keep the dependency depth
-// near 10.  NaN if a score is.
+// near 10.
 template <bool kPartial, bool kNeg>
 __device__ __forceinline__ float row_extreme(const uint64_t (&v)[64], int kv_lo, int kv_hi) {
   const float fill = kNeg ? INFINITY : -INFINITY;
@@ -519,8 +519,8 @@ __device__ __forceinline__ float row_extreme(const uint64_t (&v)[64], int kv_lo,
       a[i] = kNeg ? min3f(a[i], x0, x1) : max3f(a[i], x0, x1);
     }
   }
-  if (kNeg) return min3f(min3f(a[0], a[1], a[2]), min3f(a[3], a[4], a[5]), min3f(a[6], a[7], a[7]));
-  return max3f(max3f(a[0], a[1], a[2]), max3f(a[3], a[4], a[5]), max3f(a[6], a[7], a[7]));
+  if (kNeg) return min3f(min3f(a[0], a[1], a[2]), min3f(a[3], a[4], a[5]), fminf(a[6], a[7]));
+  return max3f(max3f(a[0], a[1], a[2]), max3f(a[3], a[4], a[5]), fmaxf(a[6], a[7]));
 }
 
 // One 128 x 128 score tile of one row (thread): row extreme, exponent-shift
@@ -530,21 +530,17 @@ __device__ __forceinline__ float row_extreme(const uint64_t (&v)[64], int kv_lo,
 // keys 64-127.  Scores stay in register pairs and use packed fp32 arithmetic.
 // With kPartial, keys outside [kv_lo, kv_hi) get weight 0: the ragged last tile
 // of a segment (kv_lo = 0), or a row's own segment inside a group tile.
-// A row with a score that is NaN or infinitely large is NaN.  Where some exponentials are polynomials (kHides), its
-// exponent shift becomes NaN and with it the others: the polynomial of a NaN is 2^-125, and the key as good as masked.
 template <bool kPartial, bool kNeg, int D>
 __device__ __forceinline__ void softmax_tile(const uint64_t (&v)[64], int kv_lo, int kv_hi, bool first, float c,
                                              uint32_t tS, uint32_t tO, float& m, float& l, float& lr,
                                              uint64_t* p_full_half, int lane) {
-  float xmax = row_extreme<kPartial, kNeg>(v, kv_lo, kv_hi) * c;  // log2 units
-  constexpr bool kHides = !kPartial && kPolyPairsPer4<D> > 0;
-  if (kHides && xmax == INFINITY) xmax = NAN;
+  const float xmax = row_extreme<kPartial, kNeg>(v, kv_lo, kv_hi) * c;  // log2 units
   bool rescale = false;  // warp-uniform
   float alpha = 1.f;
   if (first) {
     m = xmax;
-  } else if (__any_sync(0xffffffffu, kHides ? !(xmax <= m + kRescaleLog2) : xmax > m + kRescaleLog2)) {
-    const float m_new = kHides ? max3f(m, xmax, xmax) : fmaxf(m, xmax);
+  } else if (__any_sync(0xffffffffu, xmax > m + kRescaleLog2)) {
+    const float m_new = fmaxf(m, xmax);
     alpha = ex2_approx(m - m_new);
     l *= alpha;
     lr *= alpha;
@@ -606,6 +602,12 @@ __device__ __forceinline__ void softmax_tile(const uint64_t (&v)[64], int kv_lo,
   const uint64_t su2 = f2_add(su[0], su[1]), sr2 = f2_add(sr[0], sr[1]);
   l += f2_lo(su2) + f2_hi(su2);
   if (!FwdCfg<D>::kSumColumn) lr += PA_NORM_ROUNDED_D128 ? f2_lo(sr2) + f2_hi(sr2) : f2_lo(su2) + f2_hi(su2);
+}
+
+// ln of a row's sum of exponentials.  lr, the sum of the weights as bf16, is infinite where a score was NaN or infinite
+// and met a polynomial exponential (ex2x2_poly), whose fp32 value is still finite: 0 lr makes that NaN, and is 0 else.
+__device__ __forceinline__ float row_lse(float m, float l, float lr) {
+  return fmaf(0.f, lr, m + __log2f(l)) * 0.69314718055994531f;
 }
 
 template <int D>
@@ -723,8 +725,7 @@ __device__ __forceinline__ void run_softmax(const FwdParams& p, uint8_t* smem, B
     __syncwarp();
     if (lane == 0) mbar_arrive(&bars->o_empty[tile]);  // O columns may be overwritten now
     if (row_ok) {
-      const float lse2 = m + __log2f(l);
-      p.lse[static_cast<size_t>(token) * p.heads + w.head] = lse2 * 0.69314718055994531f;
+      p.lse[static_cast<size_t>(token) * p.heads + w.head] = row_lse(m, l, lr);
     }
   }
 }

@@ -394,7 +394,7 @@ __device__ __forceinline__ void sparse_softmax(const SparseFwdParams& p, SparseB
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(&bars->o_empty[tile]);
-    if (row_ok) p.lse[at] = (m + __log2f(l)) * 0.69314718055994531f;
+    if (row_ok) p.lse[at] = row_lse(m, l, lr);
   }
 }
 

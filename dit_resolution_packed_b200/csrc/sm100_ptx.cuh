@@ -484,15 +484,15 @@ __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
-// Three-input max / min (sm_100); NaN if one of them is.
+// Three-input max / min (sm_100).
 __device__ __forceinline__ float max3f(float a, float b, float c) {
   float d;
-  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
 __device__ __forceinline__ float min3f(float a, float b, float c) {
   float d;
-  asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
 
@@ -513,7 +513,9 @@ __device__ __forceinline__ uint64_t ex2x2(uint64_t x) {
 // then 2^f by the degree-3 minimax polynomial of exp2_poly.cuh (Horner, packed
 // fma) and 2^n by adding n to the exponent field.  Inputs are clamped to
 // >= -125 so that 2^n stays a normal number; the result is then < 2^-124,
-// negligible against the row sum (>= 1).  Max relative error ~7.5e-5.
+// negligible against the row sum (>= 1).  Max relative error ~7.5e-5.  A NaN (as
+// arithmetic makes it: 0x7fffffff) gives 0x7f7fffff, the largest finite value, and
+// infinity as bf16: a softmax row that has one has an infinite sum, and is NaN.
 // `k` holds the pair constants: {magic, magic}, {-magic, -magic}, C0..C3 pairs.
 struct Exp2PolyConsts {
   uint64_t magic, neg_magic, c0, c1, c2, c3;
@@ -522,8 +524,8 @@ __device__ __forceinline__ uint64_t ex2x2_poly(uint64_t x, const Exp2PolyConsts&
   uint64_t y;
   asm("{\n\t.reg .f32 a, b;\n\t.reg .b64 xc, t, n, f, p;\n\t.reg .b32 tl, th, pl, ph, rl, rh;\n\t"
       "mov.b64 {a, b}, %1;\n\t"
-      "max.f32 a, a, 0fC2FA0000;\n\t"  // -125
-      "max.f32 b, b, 0fC2FA0000;\n\t"
+      "max.NaN.f32 a, a, 0fC2FA0000;\n\t"  // -125
+      "max.NaN.f32 b, b, 0fC2FA0000;\n\t"
       "mov.b64 xc, {a, b};\n\t"
       "add.rn.f32x2 t, xc, %2;\n\t"      // t = x + magic: round(x) in the low mantissa bits
       "add.rn.f32x2 n, t, %3;\n\t"       // n = round(x) as a float

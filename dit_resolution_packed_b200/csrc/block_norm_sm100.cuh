@@ -266,7 +266,7 @@ struct RowRing {
   }
 };
 
-// Waits, within a limit each, for the copies of the m rows from the current one on.  (Out of line: it never runs.)
+// Waits, within a limit each, for the copies of the m rows from the current one on.  (Out of line: only after a timeout.)
 __device__ __noinline__ void drain_rows(uint64_t* full, RingPlace at, int stages, int m, uint64_t limit_ns) {
   for (int r = 0; r < m; ++r) drain_wait(full + at.stage_of(stages, r), at.phase_of(stages, r), limit_ns);
 }

@@ -430,9 +430,9 @@ __device__ __forceinline__ void bwd_mma(const BwdParams& p, uint8_t* smem, BwdBa
   for (;;) {
     BwdItem w;
     const int got = bwd_next_item(bars, sk, wc, w);
-    if (got != -2 && leader) mbar_arrive(&bars->sched_empty[(sk - 1) & 1]);
-    if (got == -2) ok = false;
-    if (got <= 0) break;
+    ok = __all_sync(0xffffffffu, got != -2);
+    if (__any_sync(0xffffffffu, got <= 0)) break;
+    if (leader) mbar_arrive(&bars->sched_empty[(sk - 1) & 1]);  // the vote took what every lane has read
     if (kSparse && w.nq == 0) continue;
     if (!(ok = mbar_wait(&bars->kv_full, kv_round & 1u, wc))) break;
     ++kv_round;

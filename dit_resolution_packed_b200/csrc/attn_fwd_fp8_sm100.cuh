@@ -225,9 +225,9 @@ __device__ __forceinline__ void run_mma_fp8(uint8_t* smem, Bars* bars, const Wai
   for (;;) {
     WorkItem w;
     const int got = next_item_from_ring(bars, sk, wc, false, w);
-    if (got != -2 && leader) mbar_arrive(&bars->sched_empty[(sk - 1) & 1]);
-    if (got == -2) ok = false;
-    if (got <= 0) break;
+    ok = __all_sync(0xffffffffu, got != -2);
+    if (__any_sync(0xffffffffu, got <= 0)) break;
+    if (leader) mbar_arrive(&bars->sched_empty[(sk - 1) & 1]);  // the vote took what every lane has read
     if (!(ok = mbar_wait(&bars->q_full, q_round & 1u, wc))) break;
     ++q_round;
     int ks = slot;

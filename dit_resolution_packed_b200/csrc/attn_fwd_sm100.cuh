@@ -377,9 +377,9 @@ __device__ __forceinline__ void run_mma(const FwdParams& p, uint8_t* smem, Bars*
   for (;;) {
     WorkItem w;
     const int got = next_item_from_ring(bars, sk, wc, false, w);
-    if (got != -2 && leader) mbar_arrive(&bars->sched_empty[(sk - 1) & 1]);
-    if (got == -2) ok = false;
-    if (got <= 0) break;
+    ok = __all_sync(0xffffffffu, got != -2);
+    if (__any_sync(0xffffffffu, got <= 0)) break;
+    if (leader) mbar_arrive(&bars->sched_empty[(sk - 1) & 1]);  // the vote took what every lane has read
     if (w.n0) {
       // A group of short segments: S_t = Q_t K_t^T and O_t = P_t V_t, tile t meeting only
       // key tile t.  The ring holds Q_0, K_0, V_0 [, Q_1, K_1, V_1] in this order.

@@ -238,9 +238,9 @@ __device__ __forceinline__ void sparse_mma(uint8_t* smem, SparseBars* bars, cons
   for (;;) {
     SparseItem w;
     const int got = sparse_next(bars, sk, wc, w);
-    if (got != -2 && leader) mbar_arrive(&bars->sched_empty[(sk - 1) & 1]);
-    if (got == -2) ok = false;
-    if (got <= 0) break;
+    ok = __all_sync(0xffffffffu, got != -2);
+    if (__any_sync(0xffffffffu, got <= 0)) break;
+    if (leader) mbar_arrive(&bars->sched_empty[(sk - 1) & 1]);  // the vote took what every lane has read
     const int32_t n = w.steps();
     if (n == 0) continue;
     if (!(ok = mbar_wait(&bars->q_full, q_round & 1u, wc))) break;
